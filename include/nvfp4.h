@@ -389,6 +389,175 @@ NVFP4_API nvfp4_status nvfp4_gemm_lora(const uint8_t* a_codes, const uint8_t* a_
                                        int32_t epilogue, void* workspace, size_t workspace_bytes,
                                        void* stream);
 
+/* ------------------------------------------------------------ rope ------ */
+
+/* One tensor of a rotary call: `heads` heads of head_dim elements per token,
+ * element (t, h, j) at x[t * x_token_stride + h * x_head_stride + j] (strides
+ * in elements, so q and k may be views of one projection's output). */
+typedef struct nvfp4_rope_tensor {
+  const void* x;
+  void* out; /* may be x itself, with the same strides */
+  int64_t heads;
+  int64_t x_token_stride, x_head_stride;
+  int64_t out_token_stride, out_head_stride;
+} nvfp4_rope_tensor;
+
+/* Rotary positions with several axes (time, height, width of a video token).
+ *   axes, sections  the first sections[0] pairs of a head turn with axis 0, the
+ *                next sections[1] with axis 1, ... (1 to 4 axes, a section may
+ *                be 0); elements past 2 * sum(sections) are copied.
+ *   theta        pair j of an axis turns by position * theta^(-j / sections[axis])
+ *                radians (per_axis 1), pair i of all by position *
+ *                theta^(-i / sum(sections)) (per_axis 0).
+ *   interleaved  1: pair i is elements (2i, 2i + 1); 0: elements
+ *                (i, i + sum(sections)).
+ *   inverse      1: turns by the negative angle, which is the gradient: dx from
+ *                d(out). */
+typedef struct nvfp4_rope_params {
+  int32_t axes;
+  int32_t sections[4];
+  double theta;
+  int32_t interleaved;
+  int32_t per_axis;
+  int32_t inverse;
+} nvfp4_rope_params;
+
+/* Turns every pair of every tensor (n <= 8, e.g. q and k) in one launch:
+ * (x0, x1) -> (x0 cos - x1 sin, x0 sin + x1 cos) in fp32, rounded once.
+ * Angles are products in double, so far positions keep theirs.
+ *   positions  device int32 [tokens, positions_stride], one per axis (any
+ *              value, negative ones too).
+ * Shape: head_dim even, 2..512; sum(sections) <= head_dim / 2.  Alignment: two
+ * elements for pointers, even strides (wider when the strides allow: 16-byte
+ * loads).  Takes no workspace. */
+NVFP4_API nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n, int32_t dtype,
+                                  int64_t tokens, int32_t head_dim, const int32_t* positions,
+                                  int64_t positions_stride, const nvfp4_rope_params* rp,
+                                  void* stream);
+
+/* ------------------------------------------------------- 8-bit KV cache -- */
+
+/* A paged KV cache in E4M3 with one scale per page and head (a block of
+ * page_tokens tokens), for tokens that arrive one at a time or by chunks --
+ * the NVFP4 calls above quantize whole tensors.
+ *   k_codes, v_codes    device [pages, heads, page_tokens, head_dim] bytes.
+ *   k_scales, v_scales  device fp32 [pages, heads]: powers of two, 2^-40..2^40;
+ *                       value = code * scale.
+ * head_dim 64 or 128, page_tokens 32, 64 or 128; codes 16-byte aligned. */
+typedef struct nvfp4_kv8_cache {
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scales;
+  float* v_scales;
+  int64_t pages;
+  int32_t heads;
+  int32_t page_tokens;
+  int32_t head_dim;
+} nvfp4_kv8_cache;
+
+/* The sequences of a call.  Sequence s holds its tokens in the pages
+ * page_table[s * table_stride + 0], [.. + 1], ... and owns the packed rows
+ * [starts[s], starts[s + 1]) of the call's tensors; rows past starts[n] belong
+ * to none and are left as they are.
+ *   page_table  device int32, table_pages entries per sequence; entries past a
+ *               sequence's tokens are not read.
+ *   lens        device int32 [n]; its meaning is the call's.
+ *   starts      device int32 [n + 1], from any first row on, not decreasing.
+ *   rows        rows of the packed tensors.
+ *   max_rows    at least the rows of every sequence (host; sizes the launch).
+ * Device values are checked on the device: a sequence whose rows or tokens do
+ * not fit (rows, max_rows, table_pages) is skipped, and so is a page outside
+ * the cache, and NVFP4_ERR_SHAPE is recorded in the workspace error word. */
+typedef struct nvfp4_kv8_batch {
+  const int32_t* page_table;
+  int64_t table_stride;
+  int32_t table_pages;
+  const int32_t* lens;
+  const int32_t* starts;
+  int32_t n;
+  int64_t rows;
+  int32_t max_rows;
+} nvfp4_kv8_batch;
+
+/* Quantizes tokens into the cache as they are written: sequence s's packed
+ * rows of k and v become its tokens lens[s], lens[s] + 1, ...
+ * The scale of a page and head is 2^e with the smallest e that has amax <= 448
+ * * 2^e over its finite values (e in [-40, 40]; larger values and infinities
+ * saturate, NaN stays NaN).  A page that holds earlier tokens of the sequence
+ * (lens[s] inside it) keeps the larger of its scale and the new tokens'; when
+ * it grows, the earlier codes are brought to it (exact but for codes that
+ * become subnormal, which round again).  A page whose first token is written
+ * starts over.  Tokens before lens[s] and after the new ones keep their codes
+ * otherwise.
+ *   k, v  device [rows, heads, head_dim] of dtype, strides in elements, 16-byte
+ *         aligned rows.
+ * A page may be written for one sequence only in a call (shared prefix pages
+ * are read-only).  Deterministic; no atomics.
+ * Workspace: nvfp4_workspace_bytes(0) (the device error word). */
+NVFP4_API nvfp4_status nvfp4_kv8_write(const nvfp4_kv8_cache* cache, const nvfp4_kv8_batch* batch,
+                                       int32_t dtype, const void* k, int64_t k_token_stride,
+                                       int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                                       int64_t v_head_stride, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/* Reads tokens back: sequence s's tokens lens[s], lens[s] + 1, ... become its
+ * packed rows of k and v, code * scale rounded to dtype.  Arguments as
+ * nvfp4_kv8_write (k and v are outputs; the cache is only read). */
+NVFP4_API nvfp4_status nvfp4_kv8_read(const nvfp4_kv8_cache* cache, const nvfp4_kv8_batch* batch,
+                                      int32_t dtype, void* k, int64_t k_token_stride,
+                                      int64_t k_head_stride, void* v, int64_t v_token_stride,
+                                      int64_t v_head_stride, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/* Queries of an attention call.
+ *   q, out   device bf16 [rows, q_heads, head_dim], strides in elements
+ *            (multiples of 8), 16-byte aligned; q_heads a multiple of the
+ *            cache's heads (query head h reads KV head h / (q_heads / heads)).
+ *   lse      device fp32 [rows, q_heads] or NULL: log of the sum of the
+ *            exponentials (natural), -infinity for a row that sees nothing.
+ *   scale    of the scores, > 0 (1 / sqrt(head_dim) as a rule).
+ *   causal   1: a query sees the tokens up to its own; the n queries of a
+ *            sequence are its last n tokens, lens[s] - n .. lens[s] - 1.
+ *   window   >= 0: only tokens at most `window` before the query's own (and
+ *            the first `sink` tokens); -1: no window. */
+typedef struct nvfp4_kv8_query {
+  const void* q;
+  void* out;
+  float* lse;
+  int32_t q_heads;
+  int64_t q_token_stride, q_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  float scale;
+  int32_t causal;
+  int32_t window;
+  int32_t sink;
+} nvfp4_kv8_query;
+
+/* Attention over the 8-bit cache, from one query per sequence to chunks:
+ *   out = softmax(scale q K^T) V over the tokens a query sees, lens[s] = the
+ *   sequence's tokens in the cache (the queries' own among them).
+ * The codes enter the matrix products as they are (fp16, exact), the scales in
+ * fp32 beside them; scores, maxima and sums in fp32; the softmax weights are
+ * rounded to fp16 for the product with V.  A query that sees nothing gets
+ * zeros.  Codes that no query of a tile sees are never used, whatever they are;
+ * a NaN among a token's values may reach queries of the same call that do not
+ * see that token when others of the same 128-row tile do.
+ * Workspace: nvfp4_kv8_attention_workspace_bytes, 16-byte aligned (the error
+ * word, zero at first, and partial results of key ranges, joined in the order
+ * of the keys: the result is deterministic).  One call in flight per
+ * workspace. */
+NVFP4_API nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache,
+                                           const nvfp4_kv8_batch* batch,
+                                           const nvfp4_kv8_query* query, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of nvfp4_kv8_attention for these sizes (n, max_rows and
+ * table_pages as in the batch). */
+NVFP4_API size_t nvfp4_kv8_attention_workspace_bytes(int32_t heads, int32_t head_dim,
+                                                     int32_t page_tokens, int32_t q_heads,
+                                                     int32_t n, int32_t max_rows,
+                                                     int32_t table_pages);
+
 /* ------------------------------------------------------------ RHT ------- */
 
 /* Standalone 16-point RHT, y = 1/4 H16 diag(s) x on every 16-group along

@@ -2,8 +2,9 @@
 
 The compute lives in libnvfp4.so (see include/nvfp4.h).  This package holds
 the ctypes binding (``capi``), torch-facing helpers that allocate outputs with
-torch and marshal pointers and streams (below), the build step (``build``)
-and the seeded input generator (``synth``).  Importing the package does not
+torch and marshal pointers and streams (below, and ``attention`` for rotary
+positions and the 8-bit KV cache), the build step (``build``) and the seeded
+input generator (``synth``).  Importing the package does not
 load the library; the first call does, and fails loudly if it is missing.
 """
 from __future__ import annotations
@@ -18,7 +19,9 @@ from .capi import (NVFP4_BF16, NVFP4_EPI_AMAX, NVFP4_EPI_GELU_TANH, NVFP4_EPI_NO
 __all__ = ["QTensor", "quantize_1d", "quantize_2d", "global_scale", "quantize_1d_batched",
            "quantize_mixed", "gemm_lora",
            "dequantize", "dequantize_rows", "window_row_ranges", "transpose_2d", "gemm", "rht16", "workspace",
-           "device_error", "capi"]
+           "device_error", "capi",
+           "rope", "KV8Cache", "kv8_cache", "kv8_write", "kv8_read", "kv8_attention",
+           "kv8_attention_workspace"]
 
 
 def _torch():
@@ -318,3 +321,7 @@ def device_error(ws, stream=None) -> int:
     st, v = capi.nvfp4_get_device_error(ws.data_ptr(), _stream(stream))
     capi.check("nvfp4_get_device_error", st)
     return v
+
+
+from .attention import (KV8Cache, kv8_attention, kv8_attention_workspace, kv8_cache,  # noqa: E402
+                        kv8_read, kv8_write, rope)

@@ -27,6 +27,8 @@ EXPORTED = [
     "nvfp4_gemm", "nvfp4_rht16", "nvfp4_get_device_error", "nvfp4_status_string",
     "nvfp4_convert_sweep", "nvfp4_set_wait_limit", "nvfp4_set_test_stall",
     "nvfp4_lora_scratch_bytes", "nvfp4_gemm_lora", "nvfp4_gemm_workspace_bytes",
+    "nvfp4_rope", "nvfp4_kv8_write", "nvfp4_kv8_read", "nvfp4_kv8_attention",
+    "nvfp4_kv8_attention_workspace_bytes",
 ]
 
 
@@ -43,6 +45,40 @@ class nvfp4_tensor_desc(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64)]
 
 
+class nvfp4_rope_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
+
+
+class nvfp4_rope_params(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
+                ("theta", ctypes.c_double), ("interleaved", ctypes.c_int32),
+                ("per_axis", ctypes.c_int32), ("inverse", ctypes.c_int32)]
+
+
+class nvfp4_kv8_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class nvfp4_kv8_batch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_pages", ctypes.c_int32), ("lens", ctypes.c_void_p),
+                ("starts", ctypes.c_void_p), ("n", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("max_rows", ctypes.c_int32)]
+
+
+class nvfp4_kv8_query(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("q_heads", ctypes.c_int32), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64),
+                ("out_head_stride", ctypes.c_int64), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int32), ("window", ctypes.c_int32), ("sink", ctypes.c_int32)]
+
+
 class NVFP4Error(RuntimeError):
     def __init__(self, fn, status):
         self.status = status
@@ -54,6 +90,9 @@ _V, _I32, _I64, _U32, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ct
                              ctypes.c_size_t)
 _QP = ctypes.POINTER(nvfp4_qparams)
 _TD = ctypes.POINTER(nvfp4_tensor_desc)
+_RT, _RP = ctypes.POINTER(nvfp4_rope_tensor), ctypes.POINTER(nvfp4_rope_params)
+_KC, _KB = ctypes.POINTER(nvfp4_kv8_cache), ctypes.POINTER(nvfp4_kv8_batch)
+_KQ = ctypes.POINTER(nvfp4_kv8_query)
 
 _SIGS = {
     "nvfp4_workspace_bytes": (_SZ, [_I32]),
@@ -82,6 +121,11 @@ _SIGS = {
     "nvfp4_gemm_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
     "nvfp4_gemm_lora": (_I32, [_V, _V, _V, _V, _V, _V, _I64, _I64, _I64, _V, _I64, _V, _I64, _I64,
                                ctypes.c_float, _V, _SZ, _V, _I32, _I64, _I32, _V, _SZ, _V]),
+    "nvfp4_rope": (_I32, [_RT, _I32, _I32, _I64, _I32, _V, _I64, _RP, _V]),
+    "nvfp4_kv8_write": (_I32, [_KC, _KB, _I32, _V, _I64, _I64, _V, _I64, _I64, _V, _SZ, _V]),
+    "nvfp4_kv8_read": (_I32, [_KC, _KB, _I32, _V, _I64, _I64, _V, _I64, _I64, _V, _SZ, _V]),
+    "nvfp4_kv8_attention": (_I32, [_KC, _KB, _KQ, _V, _SZ, _V]),
+    "nvfp4_kv8_attention_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32]),
 }
 
 
@@ -209,6 +253,34 @@ def nvfp4_set_wait_limit(ns):
 
 def nvfp4_set_test_stall(on):
     return _call("nvfp4_set_test_stall", on)
+
+
+def nvfp4_rope(tensors, n, dtype, tokens, head_dim, positions, positions_stride, rp, stream):
+    return _call("nvfp4_rope", tensors, n, dtype, tokens, head_dim, positions, positions_stride,
+                 ctypes.byref(rp), stream)
+
+
+def nvfp4_kv8_write(cache, batch, dtype, k, k_token, k_head, v, v_token, v_head, ws, ws_bytes,
+                    stream):
+    return _call("nvfp4_kv8_write", ctypes.byref(cache), ctypes.byref(batch), dtype, k, k_token,
+                 k_head, v, v_token, v_head, ws, ws_bytes, stream)
+
+
+def nvfp4_kv8_read(cache, batch, dtype, k, k_token, k_head, v, v_token, v_head, ws, ws_bytes,
+                   stream):
+    return _call("nvfp4_kv8_read", ctypes.byref(cache), ctypes.byref(batch), dtype, k, k_token,
+                 k_head, v, v_token, v_head, ws, ws_bytes, stream)
+
+
+def nvfp4_kv8_attention(cache, batch, query, ws, ws_bytes, stream):
+    return _call("nvfp4_kv8_attention", ctypes.byref(cache), ctypes.byref(batch),
+                 ctypes.byref(query), ws, ws_bytes, stream)
+
+
+def nvfp4_kv8_attention_workspace_bytes(heads, head_dim, page_tokens, q_heads, n, max_rows,
+                                        table_pages):
+    return _call("nvfp4_kv8_attention_workspace_bytes", heads, head_dim, page_tokens, q_heads, n,
+                 max_rows, table_pages)
 
 
 def nvfp4_status_string(s):

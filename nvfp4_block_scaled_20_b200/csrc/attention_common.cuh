@@ -1,0 +1,170 @@
+// What the two attention kernels over the 8-bit cache share: bounded mbarrier
+// waits, bulk copies, the ranges of keys a tile of query rows sees, and the
+// layout of partial results.
+//
+// The arithmetic of both, per query row i (t in units of log2):
+//
+//   t_ij = c_i (q_i . kcode_j) ks_j + log2(vs_j),   m_i = max_j t_ij
+//   w_ij = 2^(t_ij - m_i)                           (<= 2^kLazy)
+//   o_i  = sum_j w_ij vcode_j / sum_j w_ij / vs_j
+//
+// ks_j, vs_j are the scales of j's page and head.  With V's scale inside the
+// exponent the value codes enter the matrix product as they are, at no
+// operation per element, and every weight is at most 2^kLazy whatever the
+// spread of V's scales, so fp16 weights lose nothing to range; log2(vs) is a
+// whole number.  The row sum divides a page's sum of weights by vs once.  With
+// |log2 vs| <= 40 a weight that underflows fp32 (2^-126) belongs to a
+// probability below 2^-46 of the row's largest.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "attention.h"
+#include "device_common.cuh"
+
+namespace nvfp4 {
+
+constexpr uint32_t kDevErrShape = 2u;  // NVFP4_ERR_SHAPE
+// A row's maximum is replaced only when a new one is larger by more than this
+// (in log2): rescaling the accumulators is rare, and weights stay <= 2^8, far
+// inside fp16.
+constexpr float kLazy = 8.0f;
+constexpr float kNegInf = -INFINITY;
+
+// ------------------------------------------------------------ PTX wrappers
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ uint64_t global_ns() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait: false when it ran out or another role gave up.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                         uint64_t limit_ns) {
+  if (bar_try(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (bar_try(bar, parity)) return true;
+    if ((i & 63) == 0) {
+      if (gave_up && *gave_up) return false;
+      if (global_ns() - t0 > limit_ns) return false;
+    }
+  }
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two E4M3 codes -> two fp16 values (exact), the low code in the low half.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t pair) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)pair));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ------------------------------------------------------------ sequences
+struct QuerySeq {
+  int64_t first;  // first packed query row
+  int len, n;     // cached tokens, queries
+};
+__device__ __forceinline__ bool load_query_seq(const Kv8Batch& b, int page_tokens, int s,
+                                               QuerySeq& q) {
+  const int64_t r0 = b.starts[s], r1 = b.starts[s + 1];
+  q.first = r0;
+  q.len = b.lens[s];
+  q.n = (int)(r1 - r0);
+  return r0 >= 0 && r1 >= r0 && r1 <= b.rows && r1 - r0 <= b.max_rows && q.len >= 0 &&
+         q.len <= (int64_t)b.table_pages * page_tokens;
+}
+
+// Keys that query i of a sequence sees: [lo, hi) and [0, sink).
+struct Seen {
+  int lo, hi, sink;
+};
+__device__ __forceinline__ Seen seen_by(const Kv8Attention& a, const QuerySeq& q, int i) {
+  const int at = q.len - q.n + i;  // the query's place, negative before the cache's start
+  Seen s;
+  s.hi = a.causal ? max(0, min(q.len, at + 1)) : q.len;
+  s.lo = a.window >= 0 ? max(0, min(at, q.len) - a.window) : 0;
+  s.sink = a.window >= 0 ? min(a.sink, s.hi) : 0;
+  return s;
+}
+// Steps of kKeys keys that queries [i0, i1] of a sequence need: `head` steps
+// from 0 (the sink) and then those from `from` on, `total` in all.
+struct Steps {
+  int head, from, total;
+};
+template <int kKeys>
+__device__ __forceinline__ Steps steps_of(const Kv8Attention& a, const QuerySeq& q, int i0,
+                                          int i1) {
+  const Seen first = seen_by(a, q, i0), last = seen_by(a, q, i1);
+  Steps s;
+  const int end = (last.hi + kKeys - 1) / kKeys;
+  s.head = (last.sink + kKeys - 1) / kKeys;
+  s.from = max(first.lo / kKeys, s.head);
+  s.total = s.head + max(0, end - s.from);
+  return s;
+}
+__device__ __forceinline__ int step_at(const Steps& s, int i) {
+  return i < s.head ? i : s.from + (i - s.head);
+}
+
+// The power of two that brings a query row of largest magnitude amax below 4
+// (its fp16 values then keep all bits of bf16 down to 2^-24 of the row's
+// largest), as an exponent.
+__device__ __forceinline__ int row_exponent(float amax) {
+  const int e = (int)(__float_as_uint(amax) >> 23) - 127;
+  return max(-126, min(126, e));
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// ------------------------------------------------------- partial results
+// Part `i` of `kRows` rows: kRows x dim fp32 sums of w v, then, after all
+// parts, kRows pairs (m, l) each.
+template <int kRows>
+__device__ __forceinline__ float* part_rows(const Kv8Attention& a, int64_t i) {
+  return a.part + i * kRows * a.c.dim;
+}
+template <int kRows>
+__device__ __forceinline__ float2* part_stats(const Kv8Attention& a, int64_t parts, int64_t i) {
+  return reinterpret_cast<float2*>(a.part + parts * kRows * a.c.dim) + i * kRows;
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,499 @@
+// Attention of few query rows over the 8-bit paged cache, and the kernel that
+// joins partial results.
+//
+// One CTA takes 16 rows (the queries of one sequence times the query heads of
+// one KV head) and a run of 64-key steps.  What bounds it: the cache's bytes,
+// read once: 2 dim bytes per key and KV head.  So
+//   * a producer warp keeps a ring of steps in flight with untiled bulk copies
+//     -- the codes of a page and head are one contiguous block, so a step is
+//     one or two copies each of K and V -- and looks 32 pages ahead in the
+//     page table;
+//   * four warps each take 16 keys of a step with their own running maximum
+//     and sum and join once at the end;
+//   * the products run on mma.sync m16n8k16 in fp16.  The order of k inside a
+//     product is free as long as both operands agree, so a thread takes its K
+//     fragment as dim / 4 consecutive bytes of one key, and its V fragment as
+//     dim / 8 consecutive bytes of four keys: vector loads from shared memory
+//     and one conversion per pair of codes, no transposition.  16 rows are far
+//     from a tcgen05 tile of 128, and the tensor pipe is not what bounds it.
+// Long caches are cut into runs of equal length over CTAs; runs past a
+// sequence's end return at once, so ragged batches spread evenly.
+#include "attention_common.cuh"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kStepKeys = 64;
+constexpr int kDepth = 3;     // steps in flight
+constexpr int kWarps = 4;     // consumer warps
+constexpr int kRowsCta = 16;
+constexpr int kRowThreads = (kWarps + 1) * 32;
+
+struct RowsPlan {
+  int row_tiles;  // 16-row tiles per sequence and KV head
+  int splits;     // runs of keys
+  int run;        // steps per run
+};
+
+__device__ __forceinline__ void mma_f16(float d[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int kDim>
+struct RowsSmem {
+  uint8_t k[kDepth][kStepKeys * kDim];
+  uint8_t v[kDepth][kStepKeys * kDim];
+  float2 scale[kDepth][2];  // (ks, vs) of each 32 keys; vs < 0: the page is absent
+  uint64_t full[kDepth], empty[kDepth];
+  float2 stats[kWarps][kRowsCta];
+  int gave_up;
+};
+
+template <int kDim>
+__global__ void __launch_bounds__(kRowThreads)
+    attend_rows_kernel(const __grid_constant__ Kv8Attention a, const RowsPlan plan) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  RowsSmem<kDim>& sm = *reinterpret_cast<RowsSmem<kDim>*>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = blockIdx.x, head = blockIdx.y / plan.row_tiles;
+  const int tile = blockIdx.y - head * plan.row_tiles, seq = blockIdx.z;
+  const int pt = a.c.page_tokens;
+
+  QuerySeq q;
+  if (!load_query_seq(a.b, pt, seq, q)) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(a.err, kDevErrShape);
+    return;
+  }
+  const int row0 = tile * kRowsCta, rows = q.n * a.group;
+  if (row0 >= rows) return;
+  const Steps steps = steps_of<kStepKeys>(a, q, row0 / a.group,
+                                          (min(row0 + kRowsCta, rows) - 1) / a.group);
+  const int s0 = min(split * plan.run, steps.total);
+  const int s1 = min(s0 + plan.run, steps.total);
+  const int64_t parts = (int64_t)gridDim.x * gridDim.y * gridDim.z;
+  const int64_t part = ((int64_t)seq * gridDim.y + blockIdx.y) * gridDim.x + split;
+  if (s0 == s1 && plan.splits > 1) {
+    // nothing in this run: the joining kernel skips it
+    if (threadIdx.x < kRowsCta)
+      part_stats<kRowsCta>(a, parts, part)[threadIdx.x] = make_float2(kNegInf, 0.0f);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kDepth; ++i) {
+      bar_init(smem_addr(&sm.full[i]), 1);
+      bar_init(smem_addr(&sm.empty[i]), kWarps);
+    }
+    sm.gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncthreads();
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------- producer
+    const int pieces = pt < kStepKeys ? kStepKeys / pt : 1;  // copies per step
+    const int piece_keys = kStepKeys / pieces;
+    const uint32_t piece_bytes = piece_keys * kDim;
+    bool ok = true;
+    int issued = 0;
+    for (int i0 = s0; i0 < s1 && ok; i0 += 32 / pieces) {
+      // each lane: the page and scales of one coming piece
+      const int mine = i0 + lane / pieces;
+      int64_t page = -1;
+      float ks = 0.0f, vs = -1.0f;
+      if (mine < s1) {
+        const int key = step_at(steps, mine) * kStepKeys + (lane % pieces) * piece_keys;
+        // pages past the sequence's end are not looked up
+        if (key < q.len) {
+          page = a.b.table[seq * a.b.table_stride + key / pt];
+          if (page < 0 || page >= a.c.pages) {
+            atomicOr(a.err, kDevErrShape);
+            page = -1;
+          } else {
+            ks = a.c.scales[0][page * a.c.heads + head];
+            vs = a.c.scales[1][page * a.c.heads + head];
+          }
+        }
+      }
+      for (int i = i0; i < min(s1, i0 + 32 / pieces); ++i, ++issued) {
+        const int st = issued % kDepth;
+        if (lane == 0 && !bar_wait(smem_addr(&sm.empty[st]), ((issued / kDepth) & 1) ^ 1,
+                                   &sm.gave_up, a.wait_limit_ns))
+          ok = false;
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        if (!ok) break;
+        const int from = (i - i0) * pieces;
+        const bool mine_now = lane >= from && lane < from + pieces;
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, mine_now && page >= 0);
+        const uint32_t full = smem_addr(&sm.full[st]);
+        if (mine_now) {
+          const int p = lane - from;
+          const float2 sc = make_float2(ks, vs);
+          if (pieces == 1) sm.scale[st][0] = sc, sm.scale[st][1] = sc;
+          else sm.scale[st][p] = sc;
+        }
+        __syncwarp();
+        if (lane == 0) bar_expect(full, __popc(here) * 2 * piece_bytes);
+        __syncwarp();
+        if (mine_now && page >= 0) {
+          const int p = lane - from;
+          const int key = step_at(steps, i) * kStepKeys + p * piece_keys;
+          const int64_t off = ((page * a.c.heads + head) * pt + key % pt) * kDim;
+          bulk_copy(smem_addr(sm.k[st]) + p * piece_bytes, a.c.codes[0] + off, piece_bytes, full);
+          bulk_copy(smem_addr(sm.v[st]) + p * piece_bytes, a.c.codes[1] + off, piece_bytes, full);
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) {
+      if (lane == 0) {
+        *(volatile int*)&sm.gave_up = 1;
+        atomicOr(a.err, kDevErrTimeout);
+      }
+    }
+    // no copy may land after the CTA is gone
+    for (int j = max(0, issued - kDepth); j < issued; ++j)
+      bar_wait(smem_addr(&sm.full[j % kDepth]), (j / kDepth) & 1, nullptr, 200000000ull);
+    return;
+  }
+
+  // --------------------------------------------------------------- consumers
+  const int g = lane >> 2, c = lane & 3;
+  constexpr int kPer = kDim / 4;  // elements of a row per thread
+  uint32_t qf[kDim / 16][4];      // fragments: k-step s holds elements c * kPer + 4 s + {0..3}
+  float crow[2];
+  Seen see[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r = row0 + g + 8 * h;
+    const bool live = r < rows;
+    const int i = live ? r / a.group : 0;
+    see[h] = seen_by(a, q, i);
+    if (!live) see[h].hi = see[h].sink = 0;
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                               (q.first + i) * a.q_token +
+                               (int64_t)(head * a.group + (live ? r - i * a.group : 0)) * a.q_head +
+                               c * kPer;
+    uint32_t w[kPer / 2];
+#pragma unroll
+    for (int j = 0; j < kPer / 8; ++j) {
+      const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0, 0, 0, 0);
+      w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kPer / 2; ++j)
+      m = max(m, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    const int e = row_exponent(__uint_as_float(m));
+    const float down = pow2(-e);
+    crow[h] = a.scale_log2 * pow2(e);
+#pragma unroll
+    for (int s = 0; s < kDim / 16; ++s)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const uint32_t x = w[2 * s + p];
+        qf[s][h + 2 * p] =
+            f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down);
+      }
+  }
+  float o[kDim / 8][4];
+#pragma unroll
+  for (int t = 0; t < kDim / 8; ++t)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[t][j] = 0.0f;
+  float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
+  // what any row of the tile sees
+  const Seen first = seen_by(a, q, row0 / a.group);
+  const Seen last = seen_by(a, q, (min(row0 + kRowsCta, rows) - 1) / a.group);
+
+  bool ok = true;
+  for (int i = s0; i < s1; ++i) {
+    const int st = (i - s0) % kDepth;
+    if (!bar_wait(smem_addr(&sm.full[st]), ((i - s0) / kDepth) & 1, &sm.gave_up, a.wait_limit_ns)) {
+      ok = false;
+      break;
+    }
+    const int key0 = step_at(steps, i) * kStepKeys + warp * 16;  // this warp's 16 keys
+    const float2 sc = sm.scale[st][warp >> 1];
+    const bool absent = sc.y < 0.0f;
+    // scores of keys key0 + 8 nt + (2c, 2c + 1) for rows g and g + 8
+    float s[2][4];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+      const uint8_t* kr = sm.k[st] + (warp * 16 + nt * 8 + g) * kDim + c * kPer;
+#pragma unroll
+      for (int j = 0; j < kPer / 16; ++j) {
+        const uint4 x = *reinterpret_cast<const uint4*>(kr + 16 * j);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+          mma_f16(s[nt], qf[4 * j + n], e4m3x2_f16x2(w[n] & 0xFFFFu), e4m3x2_f16x2(w[n] >> 16));
+      }
+    }
+    const float lv = absent ? 0.0f : (float)((int)(__float_as_uint(sc.y) >> 23) - 127);
+    float top[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float f = crow[h] * sc.x;
+      top[h] = kNegInf;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int key = key0 + nt * 8 + 2 * c + j;
+          float& x = s[nt][2 * h + j];
+          const bool sees = !absent && ((key >= see[h].lo && key < see[h].hi) || key < see[h].sink);
+          x = sees ? fmaf(x, f, lv) : kNegInf;
+          top[h] = fmaxf(top[h], x);
+        }
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 1));
+      top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 2));
+    }
+    if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kLazy || top[1] > m[1] + kLazy)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float next = fmaxf(m[h], top[h]);
+        // a row that has seen nothing yet keeps -inf; nothing to rescale
+        const float f = m[h] == kNegInf ? 0.0f : exp2_approx(m[h] - next);
+        m[h] = next;
+        l[h] *= f;
+#pragma unroll
+        for (int t = 0; t < kDim / 8; ++t) o[t][2 * h] *= f, o[t][2 * h + 1] *= f;
+      }
+    }
+    const float inv = absent ? 0.0f : 1.0f / sc.y;
+    uint32_t pf[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float base = m[h] == kNegInf ? 0.0f : m[h];
+      float sum = 0.0f;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const float p0 = exp2_approx(s[nt][2 * h] - base), p1 = exp2_approx(s[nt][2 * h + 1] - base);
+        sum += p0 + p1;
+        pf[h + 2 * nt] = f16x2(p0, p1);
+      }
+      l[h] = fmaf(sum, inv, l[h]);
+    }
+    // V of keys 2c, 2c + 1 (and + 8), bytes g * kDim / 8 of each
+    constexpr int kVWords = kDim / 32;
+    uint32_t v[4][kVWords];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = 2 * c + (k & 1) + 8 * (k >> 1);
+      const uint8_t* vr = sm.v[st] + (warp * 16 + at) * kDim + g * (kDim / 8);
+      // codes that no row sees, past the sequence's end above all, may be
+      // anything, NaN among it, and 0 * NaN is not 0
+      const int key = key0 + at;
+      const bool there = !absent && ((key >= first.lo && key < last.hi) || key < last.sink);
+      if constexpr (kVWords == 4) {
+        const uint4 x = *reinterpret_cast<const uint4*>(vr);
+        v[k][0] = there ? x.x : 0u, v[k][1] = there ? x.y : 0u;
+        v[k][2] = there ? x.z : 0u, v[k][3] = there ? x.w : 0u;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2*>(vr);
+        v[k][0] = there ? x.x : 0u, v[k][1] = there ? x.y : 0u;
+      }
+    }
+    // the step's bytes are in registers: its slot may refill
+    __syncwarp();
+    if (lane == 0) bar_arrive(smem_addr(&sm.empty[st]));
+#pragma unroll
+    for (int w = 0; w < kVWords; ++w) {
+      const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140);
+      const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+      const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140);
+      const uint32_t b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+      mma_f16(o[4 * w], pf, e4m3x2_f16x2(a0 & 0xFFFFu), e4m3x2_f16x2(b0 & 0xFFFFu));
+      mma_f16(o[4 * w + 1], pf, e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(b0 >> 16));
+      mma_f16(o[4 * w + 2], pf, e4m3x2_f16x2(a1 & 0xFFFFu), e4m3x2_f16x2(b1 & 0xFFFFu));
+      mma_f16(o[4 * w + 3], pf, e4m3x2_f16x2(a1 >> 16), e4m3x2_f16x2(b1 >> 16));
+    }
+  }
+  if (!ok && lane == 0) {
+    *(volatile int*)&sm.gave_up = 1;
+    atomicOr(a.err, kDevErrTimeout);
+  }
+
+  // ------------------------------------------------- join the four warps
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
+    if (c == 0) sm.stats[warp][g + 8 * h] = make_float2(m[h], l[h]);
+  }
+  // all consumer warps are done with the ring
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+  float* sums = reinterpret_cast<float*>(smem_raw);  // [kWarps][16][kDim], in the ring's place
+  static_assert(sizeof(float) * kWarps * kRowsCta * kDim <= sizeof(sm.k) + sizeof(sm.v), "fits");
+  {
+    float* mine = sums + warp * kRowsCta * kDim;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float* dst = mine + (g + 8 * h) * kDim + (2 * c + j) * (kDim / 8);
+#pragma unroll
+        for (int t = 0; t < kDim / 8; t += 4)
+          *reinterpret_cast<float4*>(dst + t) =
+              make_float4(o[t][2 * h + j], o[t + 1][2 * h + j], o[t + 2][2 * h + j],
+                          o[t + 3][2 * h + j]);
+      }
+  }
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+  const int r = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (kDim / 8);  // 8 threads per row
+  float top = kNegInf;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.stats[w][r].x);
+  float sum = 0.0f, acc[kDim / 8];
+#pragma unroll
+  for (int t = 0; t < kDim / 8; ++t) acc[t] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const float2 st = sm.stats[w][r];
+    const float f = st.x == kNegInf ? 0.0f : exp2_approx(st.x - top);
+    sum = fmaf(st.y, f, sum);
+    const float* src = sums + (w * kRowsCta + r) * kDim + d0;
+#pragma unroll
+    for (int t = 0; t < kDim / 8; ++t) acc[t] = fmaf(src[t], f, acc[t]);
+  }
+  if (row0 + r >= rows) return;
+  if (plan.splits > 1) {
+    float* dst = part_rows<kRowsCta>(a, part) + r * kDim + d0;
+#pragma unroll
+    for (int t = 0; t < kDim / 8; t += 4)
+      *reinterpret_cast<float4*>(dst + t) = make_float4(acc[t], acc[t + 1], acc[t + 2], acc[t + 3]);
+    if ((threadIdx.x & 7) == 0) part_stats<kRowsCta>(a, parts, part)[r] = make_float2(top, sum);
+    return;
+  }
+  const int i = (row0 + r) / a.group;
+  const int qh = head * a.group + (row0 + r) - i * a.group;
+  // a row that sees nothing has sum 0: zeros (a NaN sum stays)
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (q.first + i) * a.out_token +
+                       (int64_t)qh * a.out_head + d0;
+#pragma unroll
+  for (int t = 0; t < kDim / 8; t += 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 h =
+          __floats2bfloat162_rn(acc[t + 2 * j] * f, acc[t + 2 * j + 1] * f);
+      w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(dst + t) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if (a.lse && (threadIdx.x & 7) == 0)
+    a.lse[(q.first + i) * a.q_heads + qh] =
+        sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+// Joins the parts of each row, in the order of the keys (so the result does
+// not depend on which CTA finished first): one warp per row.
+template <int kRows>
+__global__ void __launch_bounds__(256)
+    join_kernel(const __grid_constant__ Kv8Attention a, int tiles, int splits) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int seq = blockIdx.z, head = blockIdx.y;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  QuerySeq q;
+  if (!load_query_seq(a.b, a.c.page_tokens, seq, q) || row >= q.n * a.group) return;
+  const int64_t parts = (int64_t)splits * tiles * a.c.heads * gridDim.z;
+  const int64_t part0 = ((int64_t)(seq * a.c.heads + head) * tiles + row / kRows) * splits;
+  const int r = row % kRows, dim = a.c.dim;
+  float top = kNegInf;
+  for (int s = lane; s < splits; s += 32)
+    top = fmaxf(top, part_stats<kRows>(a, parts, part0 + s)[r].x);
+#pragma unroll
+  for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+  float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int d0 = lane * (dim / 32);
+  for (int s = 0; s < splits; ++s) {
+    const float2 st = part_stats<kRows>(a, parts, part0 + s)[r];
+    if (st.x == kNegInf && st.y == 0.0f) continue;  // nothing seen (a NaN sum is not skipped)
+    const float f = st.x == kNegInf ? 1.0f : exp2_approx(st.x - top);
+    sum = fmaf(st.y, f, sum);
+    const float* src = part_rows<kRows>(a, part0 + s) + r * dim + d0;
+    if (dim == 128) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
+      acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
+    }
+  }
+  const int i = row / a.group, qh = head * a.group + row - i * a.group;
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
+      static_cast<__nv_bfloat16*>(a.out) + (q.first + i) * a.out_token + (int64_t)qh * a.out_head +
+      d0);
+  dst[0] = __floats2bfloat162_rn(acc[0] * f, acc[1] * f);
+  if (dim == 128) dst[1] = __floats2bfloat162_rn(acc[2] * f, acc[3] * f);
+  if (a.lse && lane == 0)
+    a.lse[(q.first + i) * a.q_heads + qh] =
+        sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+RowsPlan plan_rows(int32_t heads, int32_t group, int32_t n, int32_t max_rows, int64_t max_len) {
+  RowsPlan p;
+  p.row_tiles = (int)(((int64_t)max_rows * group + kRowsCta - 1) / kRowsCta);
+  const int64_t steps = (max_len + kStepKeys - 1) / kStepKeys;
+  // about three waves of four CTAs per SM at full length, runs of 2 to 32 steps
+  const int64_t all = (int64_t)n * heads * p.row_tiles * steps;
+  int64_t run = all / (148 * 4 * 3);
+  run = run < 2 ? 2 : (run > 32 ? 32 : run);
+  p.run = (int)run;
+  p.splits = (int)((steps + run - 1) / run);
+  if (p.splits < 1) p.splits = 1;
+  return p;
+}
+
+template <int kDim>
+cudaError_t launch_rows(const Kv8Attention& a, cudaStream_t s) {
+  const int64_t max_len = (int64_t)a.b.table_pages * a.c.page_tokens;
+  const RowsPlan p = plan_rows(a.c.heads, a.group, a.b.n, a.b.max_rows, max_len);
+  constexpr int kSmem = (int)sizeof(RowsSmem<kDim>);
+  cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<kDim>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  attend_rows_kernel<kDim><<<dim3((unsigned)p.splits, (unsigned)(a.c.heads * p.row_tiles),
+                                  (unsigned)a.b.n),
+                             kRowThreads, kSmem, s>>>(a, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.splits == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(((int64_t)a.b.max_rows * a.group + 7) / 8), (unsigned)a.c.heads,
+                     (unsigned)a.b.n);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<kRowsCta>, a, p.row_tiles, p.splits);
+}
+
+}  // namespace
+
+size_t kv8_attention_partial_bytes(int32_t heads, int32_t dim, int32_t group, int32_t n,
+                                   int32_t max_rows, int64_t max_len) {
+  const RowsPlan p = plan_rows(heads, group, n, max_rows, max_len);
+  if (p.splits == 1) return 0;
+  return (size_t)n * heads * p.row_tiles * p.splits * kRowsCta * ((size_t)dim * 4 + 8);
+}
+
+cudaError_t launch_kv8_attention(const Kv8Attention& a, cudaStream_t s) {
+  return a.c.dim == 128 ? launch_rows<128>(a, s) : launch_rows<64>(a, s);
+}
+
+}  // namespace nvfp4

@@ -1,0 +1,183 @@
+"""Refusals of the attention-side calls (rotary positions, the 8-bit cache,
+attention over it): every call here ends in host-side validation, before any
+CUDA work.  And the plain forms that the GPU tests compare with, against
+something other than themselves."""
+import math
+
+import pytest
+import torch
+
+import attention_ref as ref
+from nvfp4_block_scaled_20_b200 import build, capi
+
+A = 1 << 20  # a fake, well-aligned address: never dereferenced
+OK, INVALID, SHAPE, ALIGN, WORKSPACE = 0, 1, 2, 3, 4
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return capi.load()
+
+
+def _rope(x=A, out=A, heads=24, strides=(128 * 24, 128, 128 * 24, 128), dtype=1, tokens=4, dim=128,
+          pos=A, pos_stride=3, axes=3, sections=(22, 21, 21), theta=1e4, n=1):
+    t = (capi.nvfp4_rope_tensor * max(n, 1))()
+    for i in range(n):
+        t[i] = capi.nvfp4_rope_tensor(x, out, heads, *strides)
+    rp = capi.nvfp4_rope_params(axes, tuple(sections), theta, 1, 1, 0)
+    return capi.nvfp4_rope(t, n, dtype, tokens, dim, pos, pos_stride, rp, None)
+
+
+def test_rope_refusals():
+    assert _rope(x=None) == INVALID and _rope(out=None) == INVALID and _rope(pos=None) == INVALID
+    assert _rope(dtype=2) == INVALID and _rope(axes=0) == INVALID and _rope(axes=5) == INVALID
+    assert _rope(theta=0.0) == INVALID and _rope(theta=math.inf) == INVALID
+    assert _rope(theta=math.nan) == INVALID
+    assert _rope(dim=127) == SHAPE and _rope(dim=514) == SHAPE and _rope(tokens=-1) == SHAPE
+    assert _rope(sections=(33, 21, 21)) == SHAPE and _rope(sections=(-1, 21, 21)) == SHAPE
+    assert _rope(pos_stride=2) == SHAPE and _rope(n=9) == SHAPE and _rope(heads=-1) == SHAPE
+    assert _rope(strides=(-2, 128, 2, 128)) == SHAPE
+    assert _rope(strides=(128 * 24 + 1, 128, 128 * 24, 128)) == ALIGN
+    assert _rope(x=A + 2) == ALIGN and _rope(out=A + 2) == ALIGN and _rope(pos=A + 2) == ALIGN
+    assert _rope(x=A + 4, dtype=0) == ALIGN
+    # nothing to do
+    assert _rope(tokens=0, x=None, pos=None) == OK
+    assert _rope(heads=0, x=None) == OK and _rope(n=0) == OK
+
+
+def _cache(**kw):
+    d = dict(k_codes=A, v_codes=A, k_scales=A, v_scales=A, pages=10, heads=8, page_tokens=64,
+             head_dim=128)
+    d.update(kw)
+    return capi.nvfp4_kv8_cache(**d)
+
+
+def _batch(**kw):
+    d = dict(page_table=A, table_stride=4, table_pages=4, lens=A, starts=A, n=2, rows=6, max_rows=3)
+    d.update(kw)
+    return capi.nvfp4_kv8_batch(**d)
+
+
+BAD_CACHES = [(dict(k_codes=None), INVALID), (dict(v_scales=None), INVALID),
+              (dict(head_dim=96), SHAPE), (dict(page_tokens=16), SHAPE),
+              (dict(page_tokens=256), SHAPE), (dict(heads=0), SHAPE), (dict(heads=40000), SHAPE),
+              (dict(pages=0), SHAPE), (dict(k_codes=A + 8), ALIGN), (dict(k_scales=A + 2), ALIGN)]
+BAD_BATCHES = [(dict(page_table=None), INVALID), (dict(lens=None), INVALID),
+               (dict(starts=None), INVALID), (dict(n=-1), SHAPE), (dict(n=70000), SHAPE),
+               (dict(rows=-1), SHAPE), (dict(max_rows=-1), SHAPE), (dict(table_pages=0), SHAPE),
+               (dict(table_stride=3), SHAPE), (dict(max_rows=(1 << 30) + 1), SHAPE),
+               (dict(table_pages=1 << 25, table_stride=1 << 25), SHAPE), (dict(lens=A + 1), ALIGN)]
+
+
+@pytest.mark.parametrize("call", ["write", "read"])
+def test_cache_refusals(call):
+    fn = capi.nvfp4_kv8_write if call == "write" else capi.nvfp4_kv8_read
+    ws = capi.nvfp4_workspace_bytes(0)
+
+    def go(cache=None, batch=None, dtype=1, k=A, strides=(1024, 128, 1024, 128), v=A, w=A, wb=ws):
+        return fn(cache or _cache(), batch or _batch(), dtype, k, strides[0], strides[1], v,
+                  strides[2], strides[3], w, wb, None)
+
+    for kw, want in BAD_CACHES:
+        assert go(cache=_cache(**kw)) == want, kw
+    for kw, want in BAD_BATCHES:
+        assert go(batch=_batch(**kw)) == want, kw
+    assert go(dtype=3) == INVALID and go(k=None) == INVALID and go(v=None) == INVALID
+    assert go(k=A + 8) == ALIGN and go(strides=(1028, 128, 1024, 128)) == ALIGN
+    assert go(strides=(1024, -128, 1024, 128)) == SHAPE
+    assert go(w=None) == WORKSPACE and go(wb=ws - 1) == WORKSPACE
+    for kw in (dict(n=0), dict(rows=0), dict(max_rows=0)):
+        assert go(batch=_batch(**kw), k=None) == OK
+
+
+def test_attention_refusals():
+    need = capi.nvfp4_kv8_attention_workspace_bytes(8, 128, 64, 24, 2, 3, 4)
+
+    def go(cache=None, batch=None, w=A, wb=need, **kw):
+        d = dict(q=A, out=A, lse=None, q_heads=24, q_token_stride=24 * 128, q_head_stride=128,
+                 out_token_stride=24 * 128, out_head_stride=128, scale=0.1, causal=1, window=-1,
+                 sink=0)
+        d.update(kw)
+        return capi.nvfp4_kv8_attention(cache or _cache(), batch or _batch(),
+                                        capi.nvfp4_kv8_query(**d), w, wb, None)
+
+    for kw, want in BAD_CACHES:
+        assert go(cache=_cache(**kw)) == want, kw
+    for kw, want in BAD_BATCHES:
+        assert go(batch=_batch(**kw)) == want, kw
+    for s in (0.0, -1.0, math.inf, math.nan):
+        assert go(scale=s) == INVALID
+    assert go(causal=2) == INVALID and go(window=-2) == INVALID and go(sink=-1) == INVALID
+    assert go(q=None) == INVALID and go(out=None) == INVALID
+    assert go(q_heads=20) == SHAPE and go(q_heads=4) == SHAPE and go(q_token_stride=-8) == SHAPE
+    assert go(q=A + 8) == ALIGN and go(out=A + 2) == ALIGN and go(lse=A + 2) == ALIGN
+    assert go(q_head_stride=132) == ALIGN and go(w=A + 8) == ALIGN
+    assert go(w=None) == WORKSPACE and go(wb=need - 1) == WORKSPACE
+    assert go(batch=_batch(n=0), q=None) == OK
+
+
+def test_python_refusals():
+    import nvfp4_block_scaled_20_b200 as nv
+    with pytest.raises(ValueError):
+        nv.KV8Cache(torch.zeros(2, 3, 64, 128), torch.zeros(2, 3, 64, 128), torch.ones(2, 3),
+                    torch.ones(2, 3))
+    c = nv.kv8_cache(4, 2, 32, 64, device="cpu")
+    t = torch.zeros((1, 2), dtype=torch.int32)
+    one, two = torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    k = torch.zeros(3, 2, 64)
+    with pytest.raises(ValueError):
+        nv.kv8_write(c, k[:, :1], k, t, one, two, ws=one)
+    with pytest.raises(ValueError):
+        nv.kv8_write(c, k, k.bfloat16(), t, one, two, ws=one)
+    with pytest.raises(TypeError):
+        nv.kv8_write(c, k, k, t.long(), one, two, ws=one)
+    with pytest.raises(ValueError):
+        nv.kv8_write(c, k, k, t, one, one, ws=one)
+    with pytest.raises(TypeError):
+        nv.kv8_attention(k, c, t, one, two, ws=one)
+    with pytest.raises(ValueError):
+        nv.rope([k], torch.zeros(3, 2, dtype=torch.int64), [4, 4])
+    with pytest.raises(ValueError):
+        nv.rope([k, k[:2]], torch.zeros(3, 2, dtype=torch.int32), [4, 4])
+
+
+def test_workspace_grows_with_the_split():
+    base = capi.nvfp4_workspace_bytes(0)
+    f = capi.nvfp4_kv8_attention_workspace_bytes
+    assert f(8, 128, 64, 8, 1, 1, 1) >= base
+    assert f(8, 128, 64, 8, 1, 1, 512) > f(8, 128, 64, 8, 1, 1, 8) > base
+
+
+# ------------------------------------------------------- the plain forms
+def test_plain_e4m3_is_the_nearest_value():
+    grid = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    y = torch.cat([torch.rand(2000, dtype=torch.float64) * 500, torch.rand(2000).double() * 0.05,
+                   (grid[1:] + grid[:-1]) / 2, grid])
+    d = (y[:, None] - grid).abs()
+    near = d == d.amin(1, keepdim=True)
+    even = torch.arange(127) % 2 == 0
+    best = torch.where(near.sum(1) > 1, (near & even).double().argmax(1), near.double().argmax(1))
+    assert torch.equal(ref.e4m3(y), grid[best])
+    assert torch.equal(ref.e4m3(-y), -grid[best])
+
+
+def test_plain_rope_keeps_lengths_and_inverts():
+    x = torch.randn(5, 2, 16, dtype=torch.float64)
+    pos = torch.randint(-50, 5000, (5, 3), dtype=torch.int32)
+    for inter in (True, False):
+        y = ref.rope(x, pos, [3, 2, 2], 1e4, inter, True, False)
+        assert torch.allclose(y.norm(dim=-1), x.norm(dim=-1))
+        assert torch.allclose(ref.rope(y, pos, [3, 2, 2], 1e4, inter, True, True), x)
+        assert torch.equal(y[..., 14:], x[..., 14:])
+
+
+def test_plain_attention_against_softmax():
+    q, k, v = (torch.randn(n, 2, 8, dtype=torch.float64) for n in (3, 9, 9))
+    ok = ref.seen(3, 9, True, 4, 1, "cpu")
+    assert ok[0].tolist() == [True, False, True, True, True, True, True, False, False]
+    out, lse, _, _ = ref.attention(q, k, v, v.abs(), torch.ones(1, 2).double(), 0.3, ok)
+    for h in range(2):
+        s = (q[:, h] @ k[:, h].T * 0.3).masked_fill(~ok, -math.inf)
+        assert torch.allclose(out[:, h], torch.softmax(s, -1) @ v[:, h])
+        assert torch.allclose(lse[:, h], torch.logsumexp(s, -1))
