@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libnvfp4.so")
 OBJDIR = os.path.join(ROOT, "_build")
 SOURCES = ["quantize.cu", "gemm.cu", "api.cu", "noalloc.cu", "selfcheck.cu",
-           "api_attention.cu", "rope.cu", "kv8.cu", "kv8_attention.cu"]
+           "api_attention.cu", "rope.cu", "kv8.cu", "kv8_attention.cu",
+           "kv8_attention_tiles.cu"]
 HEADERS = ["device_common.cuh", "kernels.h", "attention.h", "attention_common.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

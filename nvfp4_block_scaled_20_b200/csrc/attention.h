@@ -82,5 +82,9 @@ struct Kv8Attention {
 size_t kv8_attention_partial_bytes(int32_t heads, int32_t dim, int32_t group, int32_t n,
                                    int32_t max_rows, int64_t max_len);
 cudaError_t launch_kv8_attention(const Kv8Attention& a, cudaStream_t s);
+// The kernel for many query rows (kv8_attention_tiles.cu), chosen by the two above.
+size_t attend_tiles_partial_bytes(int32_t heads, int32_t dim, int32_t group, int32_t n,
+                                  int32_t max_rows, int64_t max_len);
+cudaError_t launch_attend_tiles(const Kv8Attention& a, cudaStream_t s);
 
 }  // namespace nvfp4

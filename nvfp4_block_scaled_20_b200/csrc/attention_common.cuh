@@ -75,6 +75,11 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
     }
   }
 }
+// The same for a whole warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
+                                          uint64_t limit_ns) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, gave_up, limit_ns));
+}
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
   asm volatile(
@@ -165,6 +170,49 @@ __device__ __forceinline__ float* part_rows(const Kv8Attention& a, int64_t i) {
 template <int kRows>
 __device__ __forceinline__ float2* part_stats(const Kv8Attention& a, int64_t parts, int64_t i) {
   return reinterpret_cast<float2*>(a.part + parts * kRows * a.c.dim) + i * kRows;
+}
+
+// Joins the `splits` parts from part0 on of row r of a tile, in the order of
+// the keys (so the result does not depend on which CTA finished first), and
+// stores row `row` of the sequence's rows of a KV head: one warp.
+template <int kRows>
+__device__ __forceinline__ void join_row(const Kv8Attention& a, const QuerySeq& q, int64_t parts,
+                                         int64_t part0, int splits, int r, int row, int head,
+                                         int lane) {
+  const int dim = a.c.dim;
+  float top = kNegInf;
+  for (int s = lane; s < splits; s += 32)
+    top = fmaxf(top, part_stats<kRows>(a, parts, part0 + s)[r].x);
+#pragma unroll
+  for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+  float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int d0 = lane * (dim / 32);
+  for (int s = 0; s < splits; ++s) {
+    const float2 st = part_stats<kRows>(a, parts, part0 + s)[r];
+    if (st.x == kNegInf && st.y == 0.0f) continue;  // nothing seen (a NaN sum is not skipped)
+    const float f = st.x == kNegInf ? 1.0f : exp2_approx(st.x - top);
+    sum = fmaf(st.y, f, sum);
+    const float* src = part_rows<kRows>(a, part0 + s) + r * dim + d0;
+    if (dim == 128) {
+      const float4 x = *reinterpret_cast<const float4*>(src);
+      acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
+      acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2*>(src);
+      acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
+    }
+  }
+  const int i = row / a.group, qh = head * a.group + row - i * a.group;
+  // a row that sees nothing has sum 0: zeros (a NaN sum stays)
+  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
+      static_cast<__nv_bfloat16*>(a.out) + (q.first + i) * a.out_token + (int64_t)qh * a.out_head +
+      d0);
+  dst[0] = __floats2bfloat162_rn(acc[0] * f, acc[1] * f);
+  if (dim == 128) dst[1] = __floats2bfloat162_rn(acc[2] * f, acc[3] * f);
+  if (a.lse && lane == 0)
+    a.lse[(q.first + i) * a.q_heads + qh] =
+        sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace nvfp4

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kRowThreads)
   bool ok = true;
   for (int i = s0; i < s1; ++i) {
     const int st = (i - s0) % kDepth;
-    if (!bar_wait(smem_addr(&sm.full[st]), ((i - s0) / kDepth) & 1, &sm.gave_up, a.wait_limit_ns)) {
+    if (!warp_wait(smem_addr(&sm.full[st]), ((i - s0) / kDepth) & 1, &sm.gave_up, a.wait_limit_ns)) {
       ok = false;
       break;
     }
@@ -395,52 +395,18 @@ __global__ void __launch_bounds__(kRowThreads)
         sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-// Joins the parts of each row, in the order of the keys (so the result does
-// not depend on which CTA finished first): one warp per row.
-template <int kRows>
+// Joins the parts of the rows: one warp per row.
 __global__ void __launch_bounds__(256)
-    join_kernel(const __grid_constant__ Kv8Attention a, int tiles, int splits) {
+    join_rows_kernel(const __grid_constant__ Kv8Attention a, const RowsPlan plan) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
   const int seq = blockIdx.z, head = blockIdx.y;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   QuerySeq q;
   if (!load_query_seq(a.b, a.c.page_tokens, seq, q) || row >= q.n * a.group) return;
-  const int64_t parts = (int64_t)splits * tiles * a.c.heads * gridDim.z;
-  const int64_t part0 = ((int64_t)(seq * a.c.heads + head) * tiles + row / kRows) * splits;
-  const int r = row % kRows, dim = a.c.dim;
-  float top = kNegInf;
-  for (int s = lane; s < splits; s += 32)
-    top = fmaxf(top, part_stats<kRows>(a, parts, part0 + s)[r].x);
-#pragma unroll
-  for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-  float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const int d0 = lane * (dim / 32);
-  for (int s = 0; s < splits; ++s) {
-    const float2 st = part_stats<kRows>(a, parts, part0 + s)[r];
-    if (st.x == kNegInf && st.y == 0.0f) continue;  // nothing seen (a NaN sum is not skipped)
-    const float f = st.x == kNegInf ? 1.0f : exp2_approx(st.x - top);
-    sum = fmaf(st.y, f, sum);
-    const float* src = part_rows<kRows>(a, part0 + s) + r * dim + d0;
-    if (dim == 128) {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
-      acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(src);
-      acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
-    }
-  }
-  const int i = row / a.group, qh = head * a.group + row - i * a.group;
-  const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(
-      static_cast<__nv_bfloat16*>(a.out) + (q.first + i) * a.out_token + (int64_t)qh * a.out_head +
-      d0);
-  dst[0] = __floats2bfloat162_rn(acc[0] * f, acc[1] * f);
-  if (dim == 128) dst[1] = __floats2bfloat162_rn(acc[2] * f, acc[3] * f);
-  if (a.lse && lane == 0)
-    a.lse[(q.first + i) * a.q_heads + qh] =
-        sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+  const int64_t parts = (int64_t)plan.splits * plan.row_tiles * a.c.heads * gridDim.z;
+  const int64_t part0 =
+      ((int64_t)(seq * a.c.heads + head) * plan.row_tiles + row / kRowsCta) * plan.splits;
+  join_row<kRowsCta>(a, q, parts, part0, plan.splits, row % kRowsCta, row, head, threadIdx.x & 31);
 }
 
 RowsPlan plan_rows(int32_t heads, int32_t group, int32_t n, int32_t max_rows, int64_t max_len) {
@@ -480,19 +446,28 @@ cudaError_t launch_rows(const Kv8Attention& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<kRowsCta>, a, p.row_tiles, p.splits);
+  return cudaLaunchKernelEx(&cfg, join_rows_kernel, a, p);
 }
 
 }  // namespace
 
+namespace {
+// Rows of a KV head above which tiles of 256 rows on the tensor pipe are
+// faster than 16-row tiles that each read the cache.
+inline bool many_rows(int64_t max_rows, int32_t group) { return max_rows * group > 64; }
+}  // namespace
+
 size_t kv8_attention_partial_bytes(int32_t heads, int32_t dim, int32_t group, int32_t n,
                                    int32_t max_rows, int64_t max_len) {
+  if (many_rows(max_rows, group))
+    return attend_tiles_partial_bytes(heads, dim, group, n, max_rows, max_len);
   const RowsPlan p = plan_rows(heads, group, n, max_rows, max_len);
   if (p.splits == 1) return 0;
   return (size_t)n * heads * p.row_tiles * p.splits * kRowsCta * ((size_t)dim * 4 + 8);
 }
 
 cudaError_t launch_kv8_attention(const Kv8Attention& a, cudaStream_t s) {
+  if (many_rows(a.b.max_rows, a.group)) return launch_attend_tiles(a, s);
   return a.c.dim == 128 ? launch_rows<128>(a, s) : launch_rows<64>(a, s);
 }
 
