@@ -119,17 +119,21 @@ __device__ __forceinline__ bool load_query_seq(const Kv8Batch& b, int page_token
          q.len <= (int64_t)b.table_pages * page_tokens;
 }
 
-// Keys that query i of a sequence sees: [lo, hi) and [0, sink).
+// Keys that a query sees: [lo, hi) and [0, sink).  `at`: the query's place in
+// its sequence of `len` cached tokens, negative before the cache's start.
 struct Seen {
   int lo, hi, sink;
 };
-__device__ __forceinline__ Seen seen_by(const Kv8Attention& a, const QuerySeq& q, int i) {
-  const int at = q.len - q.n + i;  // the query's place, negative before the cache's start
+__device__ __forceinline__ Seen seen_at(const Kv8Attention& a, int len, int at) {
   Seen s;
-  s.hi = a.causal ? max(0, min(q.len, at + 1)) : q.len;
-  s.lo = a.window >= 0 ? max(0, min(at, q.len) - a.window) : 0;
+  s.hi = a.causal ? max(0, min(len, at + 1)) : len;
+  s.lo = a.window >= 0 ? max(0, min(at, len) - a.window) : 0;
   s.sink = a.window >= 0 ? min(a.sink, s.hi) : 0;
   return s;
+}
+// Query i of a sequence.
+__device__ __forceinline__ Seen seen_by(const Kv8Attention& a, const QuerySeq& q, int i) {
+  return seen_at(a, q.len, q.len - q.n + i);
 }
 // Steps of kKeys keys that queries [i0, i1] of a sequence need: `head` steps
 // from 0 (the sink) and then those from `from` on, `total` in all.

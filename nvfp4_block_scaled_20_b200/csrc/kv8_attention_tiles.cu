@@ -8,8 +8,8 @@
 //                 row to fp16 (a power of two out, exact) in shared memory.
 //   warps 8..11   bring K and V: 16-byte loads from the pages, E4M3 to fp16
 //                 (exact, one conversion per pair), into a ring of 128-key
-//                 tiles in the 128-byte swizzle.  The next tile's loads are
-//                 issued as the registers of this one are converted.
+//                 tiles in the 128-byte swizzle.  The next step's loads are in
+//                 flight in registers, of K and of V apart.
 //   warp 12       allocates tensor memory; one thread issues the MMAs
 //                 (tcgen05.mma.cta_group::1.kind::f16): S = Q K^T from shared
 //                 memory, O += P V with P read from tensor memory, where the
@@ -20,8 +20,6 @@
 // nothing is transposed.
 //
 // Tensor memory (columns): S / P of the halves at 0 and 128, O at 256 and 384.
-//
-// Registers: 512 threads of 128 at launch; softmax 192, loaders 80, MMA 48.
 #include <climits>
 
 #include "attention_common.cuh"
@@ -39,6 +37,12 @@ constexpr int kInfo = 4;     // ring of a step's scales
 constexpr int kTileThreads = 512;
 constexpr int kLoadWarp = 8, kMmaWarp = 12;
 constexpr uint32_t kTmemCols = 512;
+// One pair of weights in kPolyEvery takes its powers of two from the FMA pipe:
+// the special-function unit's 4 results per clock and SM quarter would take as
+// long for all of them as the tensor pipe takes for the products.
+constexpr int kPolyEvery = 4;
+constexpr float kPoly0 = 0x1.000002p+0f, kPoly1 = 0x1.62e430p-1f, kPoly2 = 0x1.ebf906p-3f,
+                kPoly3 = 0x1.c6af6cp-5f, kPoly4 = 0x1.3d1070p-7f, kPoly5 = 0x1.5f0890p-10f;
 // Tensor-memory columns of a half's scores (and weights) and sums.
 __host__ __device__ constexpr uint32_t col_s(int h) { return 128u * h; }
 __host__ __device__ constexpr uint32_t col_o(int h) { return 256u + 128u * h; }
@@ -52,7 +56,7 @@ struct TilesPlan {
 struct TilesSmem {  // after the q tiles and the ring
   float4 info[kInfo][4];  // per 32 keys of a step: ks, log2 vs, 1 / vs
   uint64_t kv_full[kSlots], kv_empty[kSlots];
-  uint64_t q_full, s_full[2], p_full[2], o_full[2], mma_done;
+  uint64_t q_full, s_full[2], p_half[2], p_full[2], o_full[2], mma_done;
   uint32_t tmem;
   int gave_up;
 };
@@ -77,26 +81,32 @@ __device__ __forceinline__ void commit(uint32_t bar) {
 // Shared-memory operand of 128-byte rows in the 128-byte swizzle: 8-row groups
 // 1024 bytes apart.  K-major: `lead` unused.  MN-major: the next 64 elements
 // of the row dimension lie `lead` bytes on.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) |
-         ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// The low word of the descriptor (address and `lead`, in 16 bytes); the high
+// word is the same for all.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead) {
+  return (addr >> 4) | ((lead >> 4) << 16);
 }
+constexpr uint32_t kOperandHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
 // kind::f16, fp16 operands (format 0), fp32 accumulator; bit 16: B is MN-major.
 __host__ __device__ constexpr uint32_t f16_instr(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t instr, uint32_t acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t instr,
+                                       uint32_t acc) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(instr), "r"(acc)
+      "{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %4, 0;\n"
+      "mov.b64 a, {%1, %5}; mov.b64 b, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(instr), "r"(acc), "r"(kOperandHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t instr, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t instr,
+                                       uint32_t acc) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(instr), "r"(acc)
+      "{ .reg .pred p; .reg .b64 b; setp.ne.b32 p, %4, 0;\n"
+      "mov.b64 b, {%2, %5};\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(instr), "r"(acc), "r"(kOperandHigh)
       : "memory");
 }
 #define NVFP4_R8(r, i) \
@@ -150,6 +160,19 @@ __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// 16 bytes, or zeros: one predicated load, no branch (which would wait for the
+// data before the next load is issued).
+__device__ __forceinline__ uint4 load_if(const void* p, bool want) {
+  uint4 v;
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %5, 0;\n"
+      "mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0;\n"
+      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4]; }"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+      : "l"(p), "r"((int)want));
+  return v;
+}
+
 // Where a 16-byte chunk of row `row` lies in a [128][64 fp16] block.
 __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
   return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
@@ -164,6 +187,40 @@ __device__ __forceinline__ void store_bf16x8(__nv_bfloat16* dst, const uint32_t*
     w[j] = *reinterpret_cast<const uint32_t*>(&h);
   }
   *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// max(a, b, c), NaN when one of them is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Two powers of two on the FMA pipe.  x = n + f, n whole, |f| <= 1/2 (adding
+// 1.5 2^23 rounds to n and leaves it in the low bits); 2^f by the polynomial of
+// degree 5 that interpolates it at the Chebyshev nodes of [-1/2, 1/2] (relative
+// error below 2.5e-7); n goes into the exponent.  x is at most 2^6 here; below
+// -125 it gives 2^-125, which no fp16 weight and no sum notices.
+__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
+  float a, b;
+  unpack2(x, a, b);
+  x = pack2(fmaxf(a, -125.0f), fmaxf(b, -125.0f));
+  const uint64_t r = add2(x, pack2(12582912.0f, 12582912.0f));
+  const uint64_t f = sub2(x, sub2(r, pack2(12582912.0f, 12582912.0f)));
+  uint64_t p = pack2(kPoly5, kPoly5);
+  p = fma2(p, f, pack2(kPoly4, kPoly4));
+  p = fma2(p, f, pack2(kPoly3, kPoly3));
+  p = fma2(p, f, pack2(kPoly2, kPoly2));
+  p = fma2(p, f, pack2(kPoly1, kPoly1));
+  p = fma2(p, f, pack2(kPoly0, kPoly0));
+  float r0, r1, p0, p1;
+  unpack2(r, r0, r1);
+  unpack2(p, p0, p1);
+  // n 2^23 + p as integers; a multiply-add, on the FMA pipe too
+  uint32_t b0, b1;
+  asm("mad.lo.u32 %0, %1, 0x800000, %2;" : "=r"(b0) : "r"(__float_as_uint(r0)), "r"(__float_as_uint(p0)));
+  asm("mad.lo.u32 %0, %1, 0x800000, %2;" : "=r"(b1) : "r"(__float_as_uint(r1)), "r"(__float_as_uint(p1)));
+  return pack2(__uint_as_float(b0), __uint_as_float(b1));
 }
 
 // A work unit: a tile, its steps, and its part (-1: the whole tile).
@@ -222,7 +279,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     s0 = (int)((int64_t)steps.total * unit.split / plan.splits);
     s1 = (int)((int64_t)steps.total * (unit.split + 1) / plan.splits);
   }
-  const int64_t parts = (int64_t)(plan.tiles - plan.full) * plan.splits;
   const int n_steps = s1 - s0;
 
   if (threadIdx.x == 0) {
@@ -233,6 +289,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     bar_init(smem_addr(&sm.q_full), 4 * halves);
     for (int h = 0; h < 2; ++h) {
       bar_init(smem_addr(&sm.s_full[h]), 1);
+      bar_init(smem_addr(&sm.p_half[h]), 4);
       bar_init(smem_addr(&sm.p_full[h]), 4);
       bar_init(smem_addr(&sm.o_full[h]), 1);
     }
@@ -256,21 +313,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (warp < kLoadWarp) {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int h = warp >> 2, r = threadIdx.x & (kHalf - 1);
-    const int row = row0 + h * kHalf + r;
-    const bool mine = row < rows;
-    const int i = mine ? row / a.group : i_first;
-    const int qh = unit.head * a.group + (mine ? row - i * a.group : 0);
     if (h < halves) {
-      Seen see = seen_by(a, q, i);
-      if (!mine) see.lo = 0, see.hi = INT_MAX;  // computed on zeros, not stored
       float crow;
+      int at;  // place of the row's query in its sequence
       {
         // the row to fp16, a power of two out
+        const int row = row0 + h * kHalf + r;
+        const bool mine = row < rows;  // the others work on zeros and store nothing
+        const int i = mine ? row / a.group : i_last;
+        at = q.len - q.n + i;
         const uint4* src = reinterpret_cast<const uint4*>(
             static_cast<const __nv_bfloat16*>(a.q) + (q.first + i) * a.q_token +
-            (int64_t)qh * a.q_head);
+            (int64_t)(unit.head * a.group + (mine ? row - i * a.group : 0)) * a.q_head);
         uint32_t w[kDim / 2];
 #pragma unroll
         for (int k = 0; k < kDim / 8; ++k) {
@@ -301,8 +356,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + col_s(h), to = tmem + lanes + col_o(h);
       // keys that every row of the warp sees
-      const int all_lo = __reduce_max_sync(0xFFFFFFFFu, see.lo);
-      const int all_hi = __reduce_min_sync(0xFFFFFFFFu, see.hi);
+      const int all_lo = seen_at(a, q.len, __reduce_max_sync(0xFFFFFFFFu, at)).lo;
+      const int all_hi = seen_at(a, q.len, __reduce_min_sync(0xFFFFFFFFu, at)).hi;
       float m = kNegInf, l = 0.0f;
       bool ok = true;
       for (int j = 0; j < n_steps; ++j) {
@@ -312,37 +367,55 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           break;
         }
         fence_after();
-        uint32_t s[kKeys];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) ld32(ts + 32 * c, s + 32 * c);
-        ld_wait<kKeys>(s);
-        if (key0 < all_lo || key0 + kKeys > all_hi) {
-#pragma unroll
-          for (int k = 0; k < kKeys; ++k) {
-            const int key = key0 + k;
-            if (!((key >= see.lo && key < see.hi) || key < see.sink))
-              s[k] = __float_as_uint(kNegInf);
-          }
-        }
+        const bool masked = key0 < all_lo || key0 + kKeys > all_hi;
         const float4* info = sm.info[j % kInfo];
-        float f[4], lv[4], inv[4], top = kNegInf;
+        // Two passes over the scores in tensor memory, 32 columns at a time in
+        // two buffers, the next 32 on the way while these are worked on.  (All
+        // 128 in registers, unrolled, overran the instruction cache.)
+        uint32_t s0_[32], s1_[32];
+        auto hide = [&](uint32_t* s, int key) {
+          const Seen see = seen_at(a, q.len, at);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+          for (int k = 0; k < 32; ++k)
+            if (!((key + k >= see.lo && key + k < see.hi) || key + k < see.sink))
+              s[k] = __float_as_uint(kNegInf);
+        };
+        float top = kNegInf;
+        auto maximum = [&](uint32_t* s, int c) {
+          if (masked) hide(s, key0 + 32 * c);
           const float4 x = info[c];
-          // never 0: masked scores (-inf) stay -inf
-          f[c] = fmaxf(crow * x.x, 1e-37f);
-          lv[c] = x.y;
-          inv[c] = x.z;
-          float t0 = kNegInf, t1 = kNegInf;
+          float t[4];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            t0 = fmaxf(t0, __uint_as_float(s[32 * c + k]));
-            t1 = fmaxf(t1, __uint_as_float(s[32 * c + k + 1]));
-          }
-          top = fmaxf(top, fmaf(fmaxf(t0, t1), f[c], lv[c]));
+          for (int k = 0; k < 4; ++k)
+            t[k] = max3(__uint_as_float(s[8 * k]), __uint_as_float(s[8 * k + 1]),
+                        __uint_as_float(s[8 * k + 2]));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            t[k] = max3(t[k], __uint_as_float(s[8 * k + 3]), __uint_as_float(s[8 * k + 4]));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            t[k] = max3(t[k], __uint_as_float(s[8 * k + 5]), __uint_as_float(s[8 * k + 6]));
+          t[0] = max3(t[0], __uint_as_float(s[7]), __uint_as_float(s[15]));
+          t[1] = max3(t[1], __uint_as_float(s[23]), __uint_as_float(s[31]));
+          t[0] = max3(t[0], t[1], max3(t[2], t[2], t[3]));
+          // the factor is never 0: masked scores (-inf) stay -inf
+          top = max3(top, top, fmaf(t[0], fmaxf(crow * x.x, 1e-37f), x.y));
+        };
+        ld32(ts, s0_);
+        ld_wait<32>(s0_);
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          ld32(ts + 32 * (c + 1), s1_);
+          maximum(s0_, c);
+          ld_wait<32>(s1_);
+          ld32(ts + 32 * ((c + 2) & 3), s0_);  // at last the first for the second pass
+          maximum(s1_, c + 1);
+          ld_wait<32>(s0_);
         }
-        if (__any_sync(0xFFFFFFFFu, top > m + kLazy)) {
-          const float next = fmaxf(m, top);
+        // a NaN among the scores that a row sees makes its maximum, and with it
+        // the whole row, NaN
+        if (__any_sync(0xFFFFFFFFu, !(top <= m + kLazy))) {
+          const float next = max3(m, m, top);
           const float g = m == kNegInf ? 0.0f : exp2_approx(m - next);
           m = next;
           l *= g;
@@ -351,41 +424,61 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // scores were issued after them
 #pragma unroll 1
             for (int c = 0; c < kDim; c += 32) {
-              uint32_t o[32];
-              ld32(to + c, o);
-              ld_wait<32>(o);
+              ld32(to + c, s1_);
+              ld_wait<32>(s1_);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
-              st32(to + c, o);
+              for (int k = 0; k < 32; ++k) s1_[k] = __float_as_uint(__uint_as_float(s1_[k]) * g);
+              st32(to + c, s1_);
             }
           }
         }
         const float base = m == kNegInf ? 0.0f : m;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint64_t ff = pack2(f[c], f[c]), bb = pack2(lv[c] - base, lv[c] - base);
+        // the weights of 32 columns, written over scores already read
+        auto weights = [&](uint32_t* s, int c) {
+          if (masked) hide(s, key0 + 32 * c);
+          const float4 x = info[c];
+          const float f = fmaxf(crow * x.x, 1e-37f);
+          const uint64_t ff = pack2(f, f), bb = pack2(x.y - base, x.y - base);
           uint32_t p[16];
           uint64_t sum = pack2(0.0f, 0.0f);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
+            uint64_t t = fma2(pack2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ff, bb);
             float x0, x1;
-            unpack2(fma2(pack2(__uint_as_float(s[32 * c + 2 * k]),
-                               __uint_as_float(s[32 * c + 2 * k + 1])), ff, bb), x0, x1);
-            x0 = exp2_approx(x0);
-            x1 = exp2_approx(x1);
-            sum = add2(sum, pack2(x0, x1));
+            if (k % kPolyEvery == kPolyEvery - 1) {
+              t = exp2_poly(t);
+              unpack2(t, x0, x1);
+            } else {
+              unpack2(t, x0, x1);
+              x0 = exp2_approx(x0);
+              x1 = exp2_approx(x1);
+              t = pack2(x0, x1);
+            }
+            sum = add2(sum, t);
             p[k] = f16x2(x0, x1);
           }
           st16(ts + 16 * c, p);
           float a0, a1;
           unpack2(sum, a0, a1);
-          l = fmaf(a0 + a1, inv[c], l);
+          l = fmaf(a0 + a1, x.z, l);
+        };
+#pragma unroll 1
+        for (int c = 0; c < 4; c += 2) {
+          ld32(ts + 32 * (c + 1), s1_);
+          weights(s0_, c);
+          ld_wait<32>(s1_);
+          if (c == 0) ld32(ts + 64, s0_);
+          weights(s1_, c + 1);
+          if (c == 0) ld_wait<32>(s0_);
+          // the product with V starts on the first half's weights
+          st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_addr(c == 0 ? &sm.p_half[h] : &sm.p_full[h]));
         }
-        st_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(&sm.p_full[h]));
       }
+      // nothing seen: what the polynomial gave for masked keys is no weight
+      if (m == kNegInf) l = 0.0f;
       if (ok && n_steps > 0 &&
           !warp_wait(smem_addr(&sm.o_full[h]), 0, gave_up, a.wait_limit_ns))
         ok = false;
@@ -394,9 +487,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) atomicOr(a.err, kDevErrTimeout);
       }
       fence_after();
-      const float by = unit.part >= 0 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-      if (unit.part >= 0 && mine)
-        part_stats<kTileRows>(a, parts, unit.part)[h * kHalf + r] = make_float2(m, l);
+      // the row's place again, so that it need not be kept in registers above
+      int tid = threadIdx.x, block = blockIdx.x;
+      asm volatile("" : "+r"(tid), "+r"(block)::"memory");
+      const Unit u = unit_of(a, plan, block);
+      QuerySeq qs;
+      load_query_seq(a.b, pt, u.seq, qs);
+      const int row = u.tile * kTileRows + tid;  // tid < 256: half and row
+      const bool mine = row < qs.n * a.group;
+      const int i = mine ? row / a.group : 0;
+      const int qh = u.head * a.group + row - i * a.group;
+      const float by = u.part >= 0 ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+      if (u.part >= 0 && mine) {
+        const int64_t parts = (int64_t)(plan.tiles - plan.full) * plan.splits;
+        part_stats<kTileRows>(a, parts, u.part)[tid] = make_float2(m, l);
+      }
 #pragma unroll 1
       for (int c = 0; c < kDim; c += 32) {
         uint32_t o[32];
@@ -408,15 +513,15 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
         if (!mine) continue;
-        if (unit.part >= 0) {
-          float4* dst = reinterpret_cast<float4*>(part_rows<kTileRows>(a, unit.part) +
-                                                  (h * kHalf + r) * kDim + c);
+        if (u.part >= 0) {
+          float4* dst = reinterpret_cast<float4*>(part_rows<kTileRows>(a, u.part) +
+                                                  tid * kDim + c);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
                                  __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
         } else {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (q.first + i) * a.out_token +
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (qs.first + i) * a.out_token +
                                (int64_t)qh * a.out_head + c;
           // a row that sees nothing (sum 0) is zero; a NaN sum stays
           if (l == 0.0f) {
@@ -427,51 +532,86 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           for (int k = 0; k < 4; ++k) store_bf16x8(dst + 8 * k, o + 8 * k, by);
         }
       }
-      if (a.lse && mine && unit.part < 0)
-        a.lse[(q.first + i) * a.q_heads + qh] =
+      if (a.lse && mine && u.part < 0)
+        a.lse[(qs.first + i) * a.q_heads + qh] =
             l == 0.0f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
     }
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- loaders
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     constexpr int kLanesRow = kDim / 16;             // lanes per key
     constexpr int kRowsLoad = 4 * 32 / kLanesRow;    // keys per load of the four warps
     constexpr int kLoads = kKeys / kRowsLoad;
     const int w = warp - kLoadWarp;
-    const int row = w * (32 / kLanesRow) + lane / kLanesRow, col = lane % kLanesRow;
-    const int pieces = kKeys / pt;       // pages per step
-    const int group = 32 / pieces;       // steps per look-up of pages
+    // The eight lanes of a shared-memory store phase write eight different
+    // 16-byte chunks of 128 (chunk 2 col, + 1, xor row): four columns of two
+    // rows.  The lanes' columns 4..7 go to the upper half of the warp.
+    const int row = w * (32 / kLanesRow) + (kDim == 128 ? (lane >> 2) & 3 : lane >> 2);
+    const int col = (lane & 3) + (kDim == 128 ? (lane >> 4) * 4 : 0);
+    const int pt_log = 31 - __clz(pt);            // 5, 6 or 7
+    const int step_log = 7 - pt_log;              // pages per step, as a power of two
+    const int group = 32 >> step_log;             // steps per look-up of pages
     const Seen first = seen_by(a, q, i_first), last = seen_by(a, q, i_last);
-    uint4 raw[kLoads];
-    int base = s0 - group;  // steps [base, base + group) are looked up
-    int page = -1;
+    int looked = 0;   // steps [looked, looked + group) are looked up:
+    int block = -1;   // each lane's page of them, as its block of codes
+    bool all_here = false;  // no page of the looked-up steps lies outside the cache
     float ks = 0.0f, vs = -1.0f;  // lanes 0..3: of the step's 32-key groups
     auto look_up = [&](int step) {
-      base = step;
-      page = -1;
-      const int mine = step + lane / pieces;
+      looked = step;
+      block = -1;
+      bool bad = false;
+      const int mine = step + (lane >> step_log);
       if (mine < s1) {
-        const int key = step_at(steps, mine) * kKeys + (lane % pieces) * pt;
+        const int key =
+            step_at(steps, mine) * kKeys + ((lane & ((1 << step_log) - 1)) << pt_log);
         if (key < q.len) {
-          page = a.b.table[unit.seq * a.b.table_stride + key / pt];
+          const int page = a.b.table[unit.seq * a.b.table_stride + (key >> pt_log)];
           if (page < 0 || page >= a.c.pages) {
             atomicOr(a.err, kDevErrShape);
-            page = -1;
+            bad = true;
+          } else {
+            block = page;
           }
         }
       }
+      all_here = !__any_sync(0xFFFFFFFFu, bad);
     };
-    auto load = [&](int step, int which, int k) {
-      const int key = step_at(steps, step) * kKeys + k * kRowsLoad + row;
-      const int64_t pg = __shfl_sync(0xFFFFFFFFu, page, (step - base) * pieces + k * kRowsLoad / pt);
-      // codes that no row of the tile sees may be anything, NaN among it
-      const bool want = pg >= 0 && ((key >= first.lo && key < last.hi) || key < last.sink);
-      const int64_t off = ((pg * a.c.heads + unit.head) * pt + key % pt) * kDim + col * 16;
-      return want ? __ldg(reinterpret_cast<const uint4*>(a.c.codes[which] + off))
-                  : make_uint4(0, 0, 0, 0);
+    // one tile's codes: 16 bytes of kLoads keys
+    auto load = [&](uint4* raw, int step, int which) {
+      const int key0 = step_at(steps, step) * kKeys;
+      const bool whole = (key0 >= first.lo && key0 + kKeys <= last.hi) || key0 + kKeys <= last.sink;
+      const uint8_t* from = nullptr;
+      bool here = false;
+      // the next page, every 32, 64 or 128 keys
+      auto turn = [&](int k) {
+        const int pg = __shfl_sync(0xFFFFFFFFu, block,
+                                   ((step - looked) << step_log) + (k * kRowsLoad >> pt_log));
+        here = pg >= 0;
+        from = a.c.codes[which] + ((int64_t)pg * a.c.heads + unit.head) * (pt * kDim) + row * kDim +
+               col * 16;
+      };
+      if (whole && all_here) {
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) {
+          const int in_page = (k * kRowsLoad) & (pt - 1);
+          if (in_page == 0) turn(k);
+          raw[k] = __ldg(reinterpret_cast<const uint4*>(from + in_page * kDim));
+        }
+        return;
+      }
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const int in_page = (k * kRowsLoad) & (pt - 1);
+        if (in_page == 0) turn(k);
+        const int key = key0 + k * kRowsLoad + row;
+        // codes that no row of the tile sees may be anything, NaN among it
+        const bool want =
+            here && (whole || (key >= first.lo && key < last.hi) || key < last.sink);
+        raw[k] = load_if(from + in_page * kDim, want);
+      }
     };
     auto scales = [&](int step) {
-      const int pg = __shfl_sync(0xFFFFFFFFu, page, (step - base) * pieces + (lane & 3) * 32 / pt);
+      const int pg =
+          __shfl_sync(0xFFFFFFFFu, block, ((step - looked) << step_log) + ((lane & 3) * 32 >> pt_log));
       ks = 0.0f;
       vs = -1.0f;
       if (w == 0 && lane < 4 && pg >= 0) {
@@ -479,31 +619,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         vs = a.c.scales[1][(int64_t)pg * a.c.heads + unit.head];
       }
     };
-    bool ok = true;
-    if (n_steps > 0) {
-      look_up(s0);
-      scales(s0);
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) raw[k] = load(s0, 0, k);
-    }
-    for (int n = 0; n < 2 * n_steps; ++n) {
-      const int slot = n % kSlots, which = n & 1;
-      if (!warp_wait(smem_addr(&sm.kv_empty[slot]), ((n / kSlots) & 1) ^ 1, gave_up, a.wait_limit_ns)) {
-        ok = false;
-        break;
-      }
-      if (which == 0 && w == 0 && lane < 4) {
-        // an absent page: its keys' scores become -inf
-        const float lv = vs < 0.0f ? kNegInf : (float)((int)(__float_as_uint(vs) >> 23) - 127);
-        sm.info[(n >> 1) % kInfo][lane] = make_float4(ks, lv, vs < 0.0f ? 0.0f : 1.0f / vs, 0.0f);
-      }
-      const int next = s0 + ((n + 1) >> 1), next_which = (n + 1) & 1;
-      const bool more = n + 1 < 2 * n_steps;
-      if (more && next_which == 0) {
-        if (next >= base + group) look_up(next);
-        scales(next);
-      }
-      uint8_t* tile = ring + slot * kTile;
+    auto store = [&](const uint4* raw, int slot) {
+      uint8_t* to = ring + slot * kTile + (col >> 2) * kBlock;
+      const int chunk = (2 * col) & 7;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
@@ -513,19 +631,50 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           f[2 * t] = e4m3x2_f16x2(x[t] & 0xFFFFu);
           f[2 * t + 1] = e4m3x2_f16x2(x[t] >> 16);
         }
-        if (more) raw[k] = load(next, next_which, k);
-        const int at = k * kRowsLoad + row, chunk = (2 * col) & 7;
-        uint8_t* block = tile + (col >> 2) * kBlock;
-        // eight lanes write eight different chunks: the lanes of the second
-        // block start with the odd one
-        const int swap = col >> 2;
-        const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
-        *reinterpret_cast<uint4*>(block + chunk_at(at, chunk + swap)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(block + chunk_at(at, chunk + 1 - swap)) = swap ? lo : hi;
+        const int at = k * kRowsLoad + row;
+        *reinterpret_cast<uint4*>(to + chunk_at(at, chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<uint4*>(to + chunk_at(at, chunk + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(smem_addr(&sm.kv_full[slot]));
+    };
+    auto wait_slot = [&](int n) {
+      return warp_wait(smem_addr(&sm.kv_empty[n % kSlots]), ((n / kSlots) & 1) ^ 1, gave_up,
+                       a.wait_limit_ns);
+    };
+    // K and V each have a tile's loads in flight: a step's time to arrive
+    uint4 rk[kLoads], rv[kLoads];
+    bool ok = true;
+    if (n_steps > 0) {
+      look_up(s0);
+      scales(s0);
+      load(rk, s0, 0);
+      load(rv, s0, 1);
+    }
+    for (int j = 0; j < n_steps; ++j) {
+      const int next = s0 + j + 1;
+      if (!wait_slot(2 * j)) {
+        ok = false;
+        break;
+      }
+      if (w == 0 && lane < 4) {
+        // an absent page: its keys' scores become -inf
+        const float lv = vs < 0.0f ? kNegInf : (float)((int)(__float_as_uint(vs) >> 23) - 127);
+        sm.info[j % kInfo][lane] = make_float4(ks, lv, vs < 0.0f ? 0.0f : 1.0f / vs, 0.0f);
+      }
+      store(rk, (2 * j) % kSlots);
+      if (next < s1) {
+        if (next >= looked + group) look_up(next);
+        scales(next);
+        load(rk, next, 0);
+      }
+      if (!wait_slot(2 * j + 1)) {
+        ok = false;
+        break;
+      }
+      store(rv, (2 * j + 1) % kSlots);
+      if (next < s1) load(rv, next, 1);
     }
     if (!ok) {
       *gave_up = 1;
@@ -533,7 +682,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else {
     // -------------------------------------------------------------------- MMA
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
     if (warp == kMmaWarp && lane == 0) {
       constexpr uint32_t kInstrS = f16_instr(kHalf, kKeys, false);
       constexpr uint32_t kInstrO = f16_instr(kHalf, kDim, true);
@@ -543,21 +691,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         a.wait_limit_ns);
       };
       auto scores = [&](int h, int n) {  // S of half h = Q K^T with the K tile n
-        const uint64_t qa = operand(q_at + h * kTile, 16);
-        const uint64_t kb = operand(ring_at + (n % kSlots) * kTile, 16);
+        const uint32_t qa = operand(q_at + h * kTile, 16);
+        const uint32_t kb = operand(ring_at + (n % kSlots) * kTile, 16);
 #pragma unroll
         for (int k = 0; k < kDim / 16; ++k) {
-          const uint64_t step = (uint64_t)((k >> 2) * (kBlock >> 4) + (k & 3) * 2);
+          const uint32_t step = (uint32_t)((k >> 2) * (kBlock >> 4) + (k & 3) * 2);
           mma_ss(tmem + col_s(h), qa + step, kb + step, kInstrS, k > 0);
         }
         commit(smem_addr(&sm.s_full[h]));
       };
-      auto output = [&](int h, int n, bool first_step) {  // O of half h += P V with the V tile n
-        const uint64_t vb = operand(ring_at + (n % kSlots) * kTile, kBlock);
+      // O of half h += P V over 64 keys of the V tile n
+      auto output = [&](int h, int n, int part, bool first_step) {
+        const uint32_t vb = operand(ring_at + (n % kSlots) * kTile, kBlock);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tmem + col_o(h), tmem + col_s(h) + 8 * k, vb + (uint64_t)(k * (2048 >> 4)), kInstrO,
+        for (int i = 0; i < kKeys / 32; ++i) {
+          const int k = part * (kKeys / 32) + i;
+          mma_ts(tmem + col_o(h), tmem + col_s(h) + 8 * k, vb + (uint32_t)(k * (2048 >> 4)), kInstrO,
                  !first_step || k > 0);
+        }
       };
       bool ok = true;
       if (n_steps > 0) {
@@ -573,12 +724,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool more = j + 1 < n_steps;
         for (int h = 0; h < halves && ok; ++h) {
           if ((h == 0 && !wait_tile(nv)) ||
-              !bar_wait(smem_addr(&sm.p_full[h]), j & 1, gave_up, a.wait_limit_ns)) {
+              !bar_wait(smem_addr(&sm.p_half[h]), j & 1, gave_up, a.wait_limit_ns)) {
             ok = false;
             break;
           }
           fence_after();
-          output(h, nv, j == 0);
+          output(h, nv, 0, j == 0);
+          if (!bar_wait(smem_addr(&sm.p_full[h]), j & 1, gave_up, a.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          fence_after();
+          output(h, nv, 1, false);
           if (h == halves - 1) commit(smem_addr(&sm.kv_empty[nv % kSlots]));
           if (more) {
             if (h == 0 && !wait_tile(nk)) {
