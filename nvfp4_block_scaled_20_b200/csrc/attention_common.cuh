@@ -62,16 +62,19 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// Bounded wait: false when it ran out or another role gave up.
+// Bounded wait: false when it ran out or another role gave up.  The clock and
+// the flag are only looked at every 32 tries: most waits are short, and what
+// follows them waits for their latency.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int* gave_up,
                                          uint64_t limit_ns) {
-  if (bar_try(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
+  uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
     if (bar_try(bar, parity)) return true;
-    if ((i & 63) == 0) {
+    if ((i & 31) == 0) {
       if (gave_up && *gave_up) return false;
-      if (global_ns() - t0 > limit_ns) return false;
+      const uint64_t t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > limit_ns) return false;
     }
   }
 }
@@ -191,21 +194,33 @@ __device__ __forceinline__ void join_row(const Kv8Attention& a, const QuerySeq& 
   for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
   float sum = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   const int d0 = lane * (dim / 32);
-  for (int s = 0; s < splits; ++s) {
-    const float2 st = part_stats<kRows>(a, parts, part0 + s)[r];
-    if (st.x == kNegInf && st.y == 0.0f) continue;  // nothing seen (a NaN sum is not skipped)
-    const float f = st.x == kNegInf ? 1.0f : exp2_approx(st.x - top);
-    sum = fmaf(st.y, f, sum);
-    const float* src = part_rows<kRows>(a, part0 + s) + r * dim + d0;
-    if (dim == 128) {
-      const float4 x = *reinterpret_cast<const float4*>(src);
-      acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
-      acc[2] = fmaf(x.z, f, acc[2]), acc[3] = fmaf(x.w, f, acc[3]);
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(src);
-      acc[0] = fmaf(x.x, f, acc[0]), acc[1] = fmaf(x.y, f, acc[1]);
+  for (int s0 = 0; s0 < splits; s0 += 32) {
+    // each lane the factor of one part: 0 where nothing was seen (its rows are
+    // not even read, they may be unwritten), NaN where its sum is NaN
+    float f = 0.0f;
+    if (s0 + lane < splits) {
+      const float2 st = part_stats<kRows>(a, parts, part0 + s0 + lane)[r];
+      if (!(st.x == kNegInf && st.y == 0.0f)) f = st.x == kNegInf ? 1.0f : exp2_approx(st.x - top);
+      sum = fmaf(st.y, f, sum);
+    }
+    const int n = min(32, splits - s0);
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+      const float g = __shfl_sync(0xFFFFFFFFu, f, s);
+      if (g == 0.0f) continue;
+      const float* src = part_rows<kRows>(a, part0 + s0 + s) + r * dim + d0;
+      if (dim == 128) {
+        const float4 x = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(x.x, g, acc[0]), acc[1] = fmaf(x.y, g, acc[1]);
+        acc[2] = fmaf(x.z, g, acc[2]), acc[3] = fmaf(x.w, g, acc[3]);
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(x.x, g, acc[0]), acc[1] = fmaf(x.y, g, acc[1]);
+      }
     }
   }
+#pragma unroll
+  for (int k = 16; k; k >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
   const int i = row / a.group, qh = head * a.group + row - i * a.group;
   // a row that sees nothing has sum 0: zeros (a NaN sum stays)
   const float f = sum == 0.0f ? 0.0f : 1.0f / sum;

@@ -1,8 +1,8 @@
 // Attention of few query rows over the 8-bit paged cache, and the kernel that
 // joins partial results.
 //
-// One CTA takes 16 rows (the queries of one sequence times the query heads of
-// one KV head) and a run of 64-key steps.  What bounds it: the cache's bytes,
+// One CTA takes 8 or 16 rows (the queries of one sequence times the query heads
+// of one KV head) and a run of 64-key steps.  What bounds it: the cache's bytes,
 // read once: 2 dim bytes per key and KV head.  So
 //   * a producer warp keeps a ring of steps in flight with untiled bulk copies
 //     -- the codes of a page and head are one contiguous block, so a step is
@@ -10,12 +10,18 @@
 //     page table;
 //   * four warps each take 16 keys of a step with their own running maximum
 //     and sum and join once at the end;
-//   * the products run on mma.sync m16n8k16 in fp16.  The order of k inside a
-//     product is free as long as both operands agree, so a thread takes its K
-//     fragment as dim / 4 consecutive bytes of one key, and its V fragment as
-//     dim / 8 consecutive bytes of four keys: vector loads from shared memory
-//     and one conversion per pair of codes, no transposition.  16 rows are far
-//     from a tcgen05 tile of 128, and the tensor pipe is not what bounds it.
+//   * the products run on mma.sync m16n8k16 in fp16 with the keys, not the
+//     queries, along the 16: S^T = K Q^T and O^T = V^T P^T.  Eight rows fill an
+//     instruction's 8 columns, so one token's grouped heads waste little, and
+//     the accumulators of 8 rows take 32 registers.  The weights turn from one
+//     layout to the other with movmatrix.  The order of k inside a product is
+//     free as long as both operands agree, so a thread takes its K fragment as
+//     dim / 4 consecutive bytes of a key, and its V fragment as dim / 8
+//     consecutive bytes of four keys: vector loads from shared memory and one
+//     conversion per pair of codes, no transposition.  So few rows are far from
+//     a tcgen05 tile of 128, and the tensor pipe is not what bounds it;
+//   * a row's maximum is only looked for when a score exceeds the old one by
+//     2^kLazy (one vote per step), its sum only added up at the end.
 // Long caches are cut into runs of equal length over CTAs; runs past a
 // sequence's end return at once, so ragged batches spread evenly.
 #include "attention_common.cuh"
@@ -25,13 +31,13 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kStepKeys = 64;
-constexpr int kDepth = 3;     // steps in flight
+constexpr int kDepth = 4;     // steps in flight
 constexpr int kWarps = 4;     // consumer warps
-constexpr int kRowsCta = 16;
 constexpr int kRowThreads = (kWarps + 1) * 32;
 
 struct RowsPlan {
-  int row_tiles;  // 16-row tiles per sequence and KV head
+  int rows;       // of a tile, 8 or 16
+  int row_tiles;  // tiles per sequence and KV head
   int splits;     // runs of keys
   int run;        // steps per run
 };
@@ -44,19 +50,28 @@ __device__ __forceinline__ void mma_f16(float d[4], const uint32_t a[4], uint32_
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Transposes an 8 x 8 matrix of 16-bit elements held two per lane.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 template <int kDim>
 struct RowsSmem {
   uint8_t k[kDepth][kStepKeys * kDim];
   uint8_t v[kDepth][kStepKeys * kDim];
   float2 scale[kDepth][2];  // (ks, vs) of each 32 keys; vs < 0: the page is absent
   uint64_t full[kDepth], empty[kDepth];
-  float2 stats[kWarps][kRowsCta];
+  float2 stats[kWarps][16];
   int gave_up;
 };
 
-template <int kDim>
-__global__ void __launch_bounds__(kRowThreads)
+// kTiles tiles of 8 rows.
+template <int kDim, int kTiles>
+__global__ void __launch_bounds__(kRowThreads, (kTiles == 1 ? 3 : 2) + (kDim == 64))
     attend_rows_kernel(const __grid_constant__ Kv8Attention a, const RowsPlan plan) {
+  constexpr int kRowsCta = 8 * kTiles;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   RowsSmem<kDim>& sm = *reinterpret_cast<RowsSmem<kDim>*>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -164,51 +179,58 @@ __global__ void __launch_bounds__(kRowThreads)
   // --------------------------------------------------------------- consumers
   const int g = lane >> 2, c = lane & 3;
   constexpr int kPer = kDim / 4;  // elements of a row per thread
-  uint32_t qf[kDim / 16][4];      // fragments: k-step s holds elements c * kPer + 4 s + {0..3}
-  float crow[2];
-  Seen see[2];
+  // B fragments of row 8 n + g: k-step s holds elements c * kPer + 4 s + {0..3}
+  uint32_t qf[kTiles][kDim / 16][2];
+  // of rows 8 n + 2 c and + 1, as the scores lie
+  float crow[kTiles][2], m[kTiles][2], l[kTiles][2];
+  int at[kTiles][2];  // the query's place in its sequence
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = row0 + g + 8 * h;
+  for (int n = 0; n < kTiles; ++n) {
+    const int r = row0 + 8 * n + g;
     const bool live = r < rows;
-    const int i = live ? r / a.group : 0;
-    see[h] = seen_by(a, q, i);
-    if (!live) see[h].hi = see[h].sink = 0;
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                               (q.first + i) * a.q_token +
-                               (int64_t)(head * a.group + (live ? r - i * a.group : 0)) * a.q_head +
-                               c * kPer;
+    const int i = live ? r / a.group : (rows - 1) / a.group;
+    const __nv_bfloat16* src =
+        static_cast<const __nv_bfloat16*>(a.q) + (q.first + i) * a.q_token +
+        (int64_t)(head * a.group + (live ? r - i * a.group : 0)) * a.q_head + c * kPer;
     uint32_t w[kPer / 2];
 #pragma unroll
     for (int j = 0; j < kPer / 8; ++j) {
       const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0, 0, 0, 0);
       w[4 * j] = x.x, w[4 * j + 1] = x.y, w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
     }
-    uint32_t m = 0;
+    uint32_t big = 0;
 #pragma unroll
     for (int j = 0; j < kPer / 2; ++j)
-      m = max(m, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    const int e = row_exponent(__uint_as_float(m));
-    const float down = pow2(-e);
-    crow[h] = a.scale_log2 * pow2(e);
+      big = max(big, max((w[j] << 16) & 0x7FFFFFFFu, w[j] & 0x7FFF0000u));
+    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+    const int e = big ? row_exponent(__uint_as_float(big)) : 0;
+    const float down = pow2(-e), up = a.scale_log2 * pow2(e);
 #pragma unroll
     for (int s = 0; s < kDim / 16; ++s)
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         const uint32_t x = w[2 * s + p];
-        qf[s][h + 2 * p] =
+        qf[n][s][p] =
             f16x2(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xFFFF0000u) * down);
       }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      crow[n][h] = __shfl_sync(0xFFFFFFFFu, up, (2 * c + h) * 4);
+      at[n][h] = q.len - q.n + __shfl_sync(0xFFFFFFFFu, i, (2 * c + h) * 4);
+      m[n][h] = kNegInf;
+      l[n][h] = 0.0f;
+    }
   }
-  float o[kDim / 8][4];
+  // O^T: fragment t holds elements g * kDim / 8 + 2 t (and + 1) of rows 2 c, 2 c + 1
+  float o[kTiles][kDim / 16][4];
 #pragma unroll
-  for (int t = 0; t < kDim / 8; ++t)
+  for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[t][j] = 0.0f;
-  float m[2] = {kNegInf, kNegInf}, l[2] = {0.0f, 0.0f};
-  // what any row of the tile sees
+    for (int t = 0; t < kDim / 16; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[n][t][j] = 0.0f;
+  // what any row of the tile sees, and what all do
   const Seen first = seen_by(a, q, row0 / a.group);
   const Seen last = seen_by(a, q, (min(row0 + kRowsCta, rows) - 1) / a.group);
 
@@ -222,99 +244,123 @@ __global__ void __launch_bounds__(kRowThreads)
     const int key0 = step_at(steps, i) * kStepKeys + warp * 16;  // this warp's 16 keys
     const float2 sc = sm.scale[st][warp >> 1];
     const bool absent = sc.y < 0.0f;
-    // scores of keys key0 + 8 nt + (2c, 2c + 1) for rows g and g + 8
-    float s[2][4];
+    // scores of keys key0 + g and + 8 for rows 2 c, 2 c + 1
+    float s[kTiles][4];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-      const uint8_t* kr = sm.k[st] + (warp * 16 + nt * 8 + g) * kDim + c * kPer;
+    for (int n = 0; n < kTiles; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+    {
+      const uint8_t* kr = sm.k[st] + (warp * 16 + g) * kDim + c * kPer;
 #pragma unroll
       for (int j = 0; j < kPer / 16; ++j) {
         const uint4 x = *reinterpret_cast<const uint4*>(kr + 16 * j);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        const uint4 y = *reinterpret_cast<const uint4*>(kr + 8 * kDim + 16 * j);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w}, z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-          mma_f16(s[nt], qf[4 * j + n], e4m3x2_f16x2(w[n] & 0xFFFFu), e4m3x2_f16x2(w[n] >> 16));
-      }
-    }
-    const float lv = absent ? 0.0f : (float)((int)(__float_as_uint(sc.y) >> 23) - 127);
-    float top[2];
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t af[4] = {e4m3x2_f16x2(w[k] & 0xFFFFu), e4m3x2_f16x2(z[k] & 0xFFFFu),
+                                  e4m3x2_f16x2(w[k] >> 16), e4m3x2_f16x2(z[k] >> 16)};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float f = crow[h] * sc.x;
-      top[h] = kNegInf;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int key = key0 + nt * 8 + 2 * c + j;
-          float& x = s[nt][2 * h + j];
-          const bool sees = !absent && ((key >= see[h].lo && key < see[h].hi) || key < see[h].sink);
-          x = sees ? fmaf(x, f, lv) : kNegInf;
-          top[h] = fmaxf(top[h], x);
+          for (int n = 0; n < kTiles; ++n)
+            mma_f16(s[n], af, qf[n][4 * j + k][0], qf[n][4 * j + k][1]);
         }
-      top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 1));
-      top[h] = fmaxf(top[h], __shfl_xor_sync(0xFFFFFFFFu, top[h], 2));
-    }
-    if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kLazy || top[1] > m[1] + kLazy)) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float next = fmaxf(m[h], top[h]);
-        // a row that has seen nothing yet keeps -inf; nothing to rescale
-        const float f = m[h] == kNegInf ? 0.0f : exp2_approx(m[h] - next);
-        m[h] = next;
-        l[h] *= f;
-#pragma unroll
-        for (int t = 0; t < kDim / 8; ++t) o[t][2 * h] *= f, o[t][2 * h + 1] *= f;
       }
     }
-    const float inv = absent ? 0.0f : 1.0f / sc.y;
-    uint32_t pf[4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float base = m[h] == kNegInf ? 0.0f : m[h];
-      float sum = 0.0f;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const float p0 = exp2_approx(s[nt][2 * h] - base), p1 = exp2_approx(s[nt][2 * h + 1] - base);
-        sum += p0 + p1;
-        pf[h + 2 * nt] = f16x2(p0, p1);
-      }
-      l[h] = fmaf(sum, inv, l[h]);
-    }
-    // V of keys 2c, 2c + 1 (and + 8), bytes g * kDim / 8 of each
+    // V of keys 2 c, 2 c + 1 (and + 8), bytes g * kDim / 8 of each
     constexpr int kVWords = kDim / 32;
     uint32_t v[4][kVWords];
+    const bool whole = !absent && ((key0 >= first.lo && key0 + 16 <= last.hi) || key0 + 16 <= last.sink);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int at = 2 * c + (k & 1) + 8 * (k >> 1);
-      const uint8_t* vr = sm.v[st] + (warp * 16 + at) * kDim + g * (kDim / 8);
-      // codes that no row sees, past the sequence's end above all, may be
-      // anything, NaN among it, and 0 * NaN is not 0
-      const int key = key0 + at;
-      const bool there = !absent && ((key >= first.lo && key < last.hi) || key < last.sink);
+      const int in = 2 * c + (k & 1) + 8 * (k >> 1);
+      const uint8_t* vr = sm.v[st] + (warp * 16 + in) * kDim + g * (kDim / 8);
       if constexpr (kVWords == 4) {
         const uint4 x = *reinterpret_cast<const uint4*>(vr);
-        v[k][0] = there ? x.x : 0u, v[k][1] = there ? x.y : 0u;
-        v[k][2] = there ? x.z : 0u, v[k][3] = there ? x.w : 0u;
+        v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
       } else {
         const uint2 x = *reinterpret_cast<const uint2*>(vr);
-        v[k][0] = there ? x.x : 0u, v[k][1] = there ? x.y : 0u;
+        v[k][0] = x.x, v[k][1] = x.y;
+      }
+      // codes that no row sees, past the sequence's end above all, may be
+      // anything, NaN among it, and 0 * NaN is not 0
+      if (!whole) {
+        const int key = key0 + in;
+        if (absent || !((key >= first.lo && key < last.hi) || key < last.sink)) {
+#pragma unroll
+          for (int w = 0; w < kVWords; ++w) v[k][w] = 0u;
+        }
       }
     }
     // the step's bytes are in registers: its slot may refill
     __syncwarp();
     if (lane == 0) bar_arrive(smem_addr(&sm.empty[st]));
+
+    const float lv = absent ? 0.0f : (float)((int)(__float_as_uint(sc.y) >> 23) - 127);
+    const bool all_see = !absent && key0 >= last.lo && key0 + 16 <= first.hi;
+    bool higher = false;
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float f = crow[n][h] * sc.x;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float& x = s[n][2 * j + h];
+          x = fmaf(x, f, lv);
+          if (!all_see) {
+            const Seen see = seen_at(a, q.len, at[n][h]);
+            const int key = key0 + g + 8 * j;
+            if (absent || !((key >= see.lo && key < see.hi) || key < see.sink)) x = kNegInf;
+          }
+          higher |= x > m[n][h] + kLazy;
+        }
+      }
+    if (__any_sync(0xFFFFFFFFu, higher)) {
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float next = fmaxf(m[n][h], fmaxf(s[n][h], s[n][2 + h]));
+          next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, 4));
+          next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, 8));
+          next = fmaxf(next, __shfl_xor_sync(0xFFFFFFFFu, next, 16));
+          // a row that has seen nothing yet keeps -inf; nothing to rescale
+          const float f = m[n][h] == kNegInf ? 0.0f : exp2_approx(m[n][h] - next);
+          m[n][h] = next;
+          l[n][h] *= f;
+#pragma unroll
+          for (int t = 0; t < kDim / 16; ++t) o[n][t][h] *= f, o[n][t][2 + h] *= f;
+        }
+    }
+    const float inv = absent ? 0.0f : 1.0f / sc.y;
+    uint32_t pf[kTiles][2];
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n) {
+      float p[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float base = m[n][h] == kNegInf ? 0.0f : m[n][h];
+        p[h] = exp2_approx(s[n][h] - base);
+        p[2 + h] = exp2_approx(s[n][2 + h] - base);
+        l[n][h] = fmaf(p[h] + p[2 + h], inv, l[n][h]);
+      }
+      pf[n][0] = transposed(f16x2(p[0], p[1]));
+      pf[n][1] = transposed(f16x2(p[2], p[3]));
+    }
 #pragma unroll
     for (int w = 0; w < kVWords; ++w) {
       const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5140);
       const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7362);
       const uint32_t b0 = __byte_perm(v[2][w], v[3][w], 0x5140);
       const uint32_t b1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-      mma_f16(o[4 * w], pf, e4m3x2_f16x2(a0 & 0xFFFFu), e4m3x2_f16x2(b0 & 0xFFFFu));
-      mma_f16(o[4 * w + 1], pf, e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(b0 >> 16));
-      mma_f16(o[4 * w + 2], pf, e4m3x2_f16x2(a1 & 0xFFFFu), e4m3x2_f16x2(b1 & 0xFFFFu));
-      mma_f16(o[4 * w + 3], pf, e4m3x2_f16x2(a1 >> 16), e4m3x2_f16x2(b1 >> 16));
+      const uint32_t f0[4] = {e4m3x2_f16x2(a0 & 0xFFFFu), e4m3x2_f16x2(a0 >> 16),
+                              e4m3x2_f16x2(b0 & 0xFFFFu), e4m3x2_f16x2(b0 >> 16)};
+      const uint32_t f1[4] = {e4m3x2_f16x2(a1 & 0xFFFFu), e4m3x2_f16x2(a1 >> 16),
+                              e4m3x2_f16x2(b1 & 0xFFFFu), e4m3x2_f16x2(b1 >> 16)};
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) {
+        mma_f16(o[n][2 * w], f0, pf[n][0], pf[n][1]);
+        mma_f16(o[n][2 * w + 1], f1, pf[n][0], pf[n][1]);
+      }
     }
   }
   if (!ok && lane == 0) {
@@ -324,37 +370,37 @@ __global__ void __launch_bounds__(kRowThreads)
 
   // ------------------------------------------------- join the four warps
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
-    if (c == 0) sm.stats[warp][g + 8 * h] = make_float2(m[h], l[h]);
-  }
+  for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[n][h] += __shfl_xor_sync(0xFFFFFFFFu, l[n][h], 4);
+      l[n][h] += __shfl_xor_sync(0xFFFFFFFFu, l[n][h], 8);
+      l[n][h] += __shfl_xor_sync(0xFFFFFFFFu, l[n][h], 16);
+      if (g == 0) sm.stats[warp][8 * n + 2 * c + h] = make_float2(m[n][h], l[n][h]);
+    }
   // all consumer warps are done with the ring
   asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-  float* sums = reinterpret_cast<float*>(smem_raw);  // [kWarps][16][kDim], in the ring's place
+  float* sums = reinterpret_cast<float*>(smem_raw);  // [kWarps][rows][kDim], in the ring's place
   static_assert(sizeof(float) * kWarps * kRowsCta * kDim <= sizeof(sm.k) + sizeof(sm.v), "fits");
-  {
-    float* mine = sums + warp * kRowsCta * kDim;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+  for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        float* dst = mine + (g + 8 * h) * kDim + (2 * c + j) * (kDim / 8);
+    for (int h = 0; h < 2; ++h) {
+      float* dst = sums + (warp * kRowsCta + 8 * n + 2 * c + h) * kDim + g * (kDim / 8);
 #pragma unroll
-        for (int t = 0; t < kDim / 8; t += 4)
-          *reinterpret_cast<float4*>(dst + t) =
-              make_float4(o[t][2 * h + j], o[t + 1][2 * h + j], o[t + 2][2 * h + j],
-                          o[t + 3][2 * h + j]);
-      }
-  }
+      for (int t = 0; t < kDim / 16; t += 2)
+        *reinterpret_cast<float4*>(dst + 2 * t) =
+            make_float4(o[n][t][h], o[n][t][2 + h], o[n][t + 1][h], o[n][t + 1][2 + h]);
+    }
   asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-  const int r = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * (kDim / 8);  // 8 threads per row
+  constexpr int kThreadsRow = 16 / kTiles, kOut = kDim / kThreadsRow;  // threads per row, elements each
+  const int r = threadIdx.x / kThreadsRow, part_of = threadIdx.x % kThreadsRow, d0 = part_of * kOut;
   float top = kNegInf;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.stats[w][r].x);
-  float sum = 0.0f, acc[kDim / 8];
+  float sum = 0.0f, acc[kOut];
 #pragma unroll
-  for (int t = 0; t < kDim / 8; ++t) acc[t] = 0.0f;
+  for (int t = 0; t < kOut; ++t) acc[t] = 0.0f;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     const float2 st = sm.stats[w][r];
@@ -362,15 +408,19 @@ __global__ void __launch_bounds__(kRowThreads)
     sum = fmaf(st.y, f, sum);
     const float* src = sums + (w * kRowsCta + r) * kDim + d0;
 #pragma unroll
-    for (int t = 0; t < kDim / 8; ++t) acc[t] = fmaf(src[t], f, acc[t]);
+    for (int t = 0; t < kOut; t += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(src + t);
+      acc[t] = fmaf(x.x, f, acc[t]), acc[t + 1] = fmaf(x.y, f, acc[t + 1]);
+      acc[t + 2] = fmaf(x.z, f, acc[t + 2]), acc[t + 3] = fmaf(x.w, f, acc[t + 3]);
+    }
   }
   if (row0 + r >= rows) return;
   if (plan.splits > 1) {
     float* dst = part_rows<kRowsCta>(a, part) + r * kDim + d0;
 #pragma unroll
-    for (int t = 0; t < kDim / 8; t += 4)
+    for (int t = 0; t < kOut; t += 4)
       *reinterpret_cast<float4*>(dst + t) = make_float4(acc[t], acc[t + 1], acc[t + 2], acc[t + 3]);
-    if ((threadIdx.x & 7) == 0) part_stats<kRowsCta>(a, parts, part)[r] = make_float2(top, sum);
+    if (part_of == 0) part_stats<kRowsCta>(a, parts, part)[r] = make_float2(top, sum);
     return;
   }
   const int i = (row0 + r) / a.group;
@@ -380,22 +430,19 @@ __global__ void __launch_bounds__(kRowThreads)
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (q.first + i) * a.out_token +
                        (int64_t)qh * a.out_head + d0;
 #pragma unroll
-  for (int t = 0; t < kDim / 8; t += 8) {
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 h =
-          __floats2bfloat162_rn(acc[t + 2 * j] * f, acc[t + 2 * j + 1] * f);
-      w[j] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    *reinterpret_cast<uint4*>(dst + t) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int t = 0; t < kOut; t += 4) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(acc[t] * f, acc[t + 1] * f);
+    const __nv_bfloat162 y = __floats2bfloat162_rn(acc[t + 2] * f, acc[t + 3] * f);
+    *reinterpret_cast<uint2*>(dst + t) = make_uint2(*reinterpret_cast<const uint32_t*>(&x),
+                                                    *reinterpret_cast<const uint32_t*>(&y));
   }
-  if (a.lse && (threadIdx.x & 7) == 0)
+  if (a.lse && part_of == 0)
     a.lse[(q.first + i) * a.q_heads + qh] =
         sum == 0.0f ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Joins the parts of the rows: one warp per row.
+template <int kRows>
 __global__ void __launch_bounds__(256)
     join_rows_kernel(const __grid_constant__ Kv8Attention a, const RowsPlan plan) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -405,35 +452,34 @@ __global__ void __launch_bounds__(256)
   if (!load_query_seq(a.b, a.c.page_tokens, seq, q) || row >= q.n * a.group) return;
   const int64_t parts = (int64_t)plan.splits * plan.row_tiles * a.c.heads * gridDim.z;
   const int64_t part0 =
-      ((int64_t)(seq * a.c.heads + head) * plan.row_tiles + row / kRowsCta) * plan.splits;
-  join_row<kRowsCta>(a, q, parts, part0, plan.splits, row % kRowsCta, row, head, threadIdx.x & 31);
+      ((int64_t)(seq * a.c.heads + head) * plan.row_tiles + row / kRows) * plan.splits;
+  join_row<kRows>(a, q, parts, part0, plan.splits, row % kRows, row, head, threadIdx.x & 31);
 }
 
 RowsPlan plan_rows(int32_t heads, int32_t group, int32_t n, int32_t max_rows, int64_t max_len) {
   RowsPlan p;
-  p.row_tiles = (int)(((int64_t)max_rows * group + kRowsCta - 1) / kRowsCta);
+  p.rows = (int64_t)max_rows * group <= 8 ? 8 : 16;
+  p.row_tiles = (int)(((int64_t)max_rows * group + p.rows - 1) / p.rows);
   const int64_t steps = (max_len + kStepKeys - 1) / kStepKeys;
-  // about three waves of four CTAs per SM at full length, runs of 2 to 32 steps
+  // about three waves of CTAs at full length, runs of 2 to 64 steps
   const int64_t all = (int64_t)n * heads * p.row_tiles * steps;
   int64_t run = all / (148 * 4 * 3);
-  run = run < 2 ? 2 : (run > 32 ? 32 : run);
+  run = run < 2 ? 2 : (run > 64 ? 64 : run);
   p.run = (int)run;
   p.splits = (int)((steps + run - 1) / run);
   if (p.splits < 1) p.splits = 1;
   return p;
 }
 
-template <int kDim>
-cudaError_t launch_rows(const Kv8Attention& a, cudaStream_t s) {
-  const int64_t max_len = (int64_t)a.b.table_pages * a.c.page_tokens;
-  const RowsPlan p = plan_rows(a.c.heads, a.group, a.b.n, a.b.max_rows, max_len);
+template <int kDim, int kTiles>
+cudaError_t launch_rows(const Kv8Attention& a, const RowsPlan& p, cudaStream_t s) {
   constexpr int kSmem = (int)sizeof(RowsSmem<kDim>);
-  cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<kDim>,
+  cudaError_t e = cudaFuncSetAttribute(attend_rows_kernel<kDim, kTiles>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  attend_rows_kernel<kDim><<<dim3((unsigned)p.splits, (unsigned)(a.c.heads * p.row_tiles),
-                                  (unsigned)a.b.n),
-                             kRowThreads, kSmem, s>>>(a, p);
+  attend_rows_kernel<kDim, kTiles><<<dim3((unsigned)p.splits, (unsigned)(a.c.heads * p.row_tiles),
+                                          (unsigned)a.b.n),
+                                     kRowThreads, kSmem, s>>>(a, p);
   e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
   cudaLaunchConfig_t cfg = {};
@@ -446,7 +492,7 @@ cudaError_t launch_rows(const Kv8Attention& a, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_rows_kernel, a, p);
+  return cudaLaunchKernelEx(&cfg, join_rows_kernel<8 * kTiles>, a, p);
 }
 
 }  // namespace
@@ -463,12 +509,16 @@ size_t kv8_attention_partial_bytes(int32_t heads, int32_t dim, int32_t group, in
     return attend_tiles_partial_bytes(heads, dim, group, n, max_rows, max_len);
   const RowsPlan p = plan_rows(heads, group, n, max_rows, max_len);
   if (p.splits == 1) return 0;
-  return (size_t)n * heads * p.row_tiles * p.splits * kRowsCta * ((size_t)dim * 4 + 8);
+  return (size_t)n * heads * p.row_tiles * p.splits * p.rows * ((size_t)dim * 4 + 8);
 }
 
 cudaError_t launch_kv8_attention(const Kv8Attention& a, cudaStream_t s) {
   if (many_rows(a.b.max_rows, a.group)) return launch_attend_tiles(a, s);
-  return a.c.dim == 128 ? launch_rows<128>(a, s) : launch_rows<64>(a, s);
+  const RowsPlan p = plan_rows(a.c.heads, a.group, a.b.n, a.b.max_rows,
+                               (int64_t)a.b.table_pages * a.c.page_tokens);
+  if (a.c.dim == 128)
+    return p.rows == 8 ? launch_rows<128, 1>(a, p, s) : launch_rows<128, 2>(a, p, s);
+  return p.rows == 8 ? launch_rows<64, 1>(a, p, s) : launch_rows<64, 2>(a, p, s);
 }
 
 }  // namespace nvfp4

@@ -74,9 +74,14 @@ __device__ __forceinline__ void fence_before() {
 __device__ __forceinline__ void fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
+// Issued by the lane with `lead` set; the whole warp runs the code around, so
+// that addresses and descriptors stay in uniform registers.
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
+  asm volatile(
+      "{ .reg .pred e; setp.ne.b32 e, %1, 0;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(bar),
+      "r"(lead)
+      : "memory");
 }
 // Shared-memory operand of 128-byte rows in the 128-byte swizzle: 8-row groups
 // 1024 bytes apart.  K-major: `lead` unused.  MN-major: the next 64 elements
@@ -92,22 +97,28 @@ __host__ __device__ constexpr uint32_t f16_instr(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t instr,
-                                       uint32_t acc) {
+                                       uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{ .reg .pred p; .reg .b64 a, b; setp.ne.b32 p, %4, 0;\n"
+      "{ .reg .pred p, e; .reg .b64 a, b; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %6, 0;\n"
       "mov.b64 a, {%1, %5}; mov.b64 b, {%2, %5};\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p; }" ::"r"(d),
-      "r"(a), "r"(b), "r"(instr), "r"(acc), "r"(kOperandHigh)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(instr), "r"(acc), "r"(kOperandHigh), "r"(lead)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t instr,
-                                       uint32_t acc) {
+                                       uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{ .reg .pred p; .reg .b64 b; setp.ne.b32 p, %4, 0;\n"
+      "{ .reg .pred p, e; .reg .b64 b; setp.ne.b32 p, %4, 0; setp.ne.b32 e, %6, 0;\n"
       "mov.b64 b, {%2, %5};\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p; }" ::"r"(d),
-      "r"(a), "r"(b), "r"(instr), "r"(acc), "r"(kOperandHigh)
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(instr), "r"(acc), "r"(kOperandHigh), "r"(lead)
       : "memory");
+}
+// 1 in one lane of the warp.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r;
 }
 #define NVFP4_R8(r, i) \
   "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), \
@@ -682,12 +693,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else {
     // -------------------------------------------------------------------- MMA
-    if (warp == kMmaWarp && lane == 0) {
+    if (warp == kMmaWarp) {
       constexpr uint32_t kInstrS = f16_instr(kHalf, kKeys, false);
       constexpr uint32_t kInstrO = f16_instr(kHalf, kDim, true);
+      const uint32_t lead = elect();
       const uint32_t ring_at = smem_addr(ring), q_at = smem_addr(sq);
       auto wait_tile = [&](int n) {
-        return bar_wait(smem_addr(&sm.kv_full[n % kSlots]), (n / kSlots) & 1, gave_up,
+        return warp_wait(smem_addr(&sm.kv_full[n % kSlots]), (n / kSlots) & 1, gave_up,
                         a.wait_limit_ns);
       };
       auto scores = [&](int h, int n) {  // S of half h = Q K^T with the K tile n
@@ -696,9 +708,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int k = 0; k < kDim / 16; ++k) {
           const uint32_t step = (uint32_t)((k >> 2) * (kBlock >> 4) + (k & 3) * 2);
-          mma_ss(tmem + col_s(h), qa + step, kb + step, kInstrS, k > 0);
+          mma_ss(tmem + col_s(h), qa + step, kb + step, kInstrS, k > 0, lead);
         }
-        commit(smem_addr(&sm.s_full[h]));
+        commit(smem_addr(&sm.s_full[h]), lead);
       };
       // O of half h += P V over 64 keys of the V tile n
       auto output = [&](int h, int n, int part, bool first_step) {
@@ -707,16 +719,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         for (int i = 0; i < kKeys / 32; ++i) {
           const int k = part * (kKeys / 32) + i;
           mma_ts(tmem + col_o(h), tmem + col_s(h) + 8 * k, vb + (uint32_t)(k * (2048 >> 4)), kInstrO,
-                 !first_step || k > 0);
+                 !first_step || k > 0, lead);
         }
       };
       bool ok = true;
       if (n_steps > 0) {
-        ok = bar_wait(smem_addr(&sm.q_full), 0, gave_up, a.wait_limit_ns) && wait_tile(0);
+        ok = warp_wait(smem_addr(&sm.q_full), 0, gave_up, a.wait_limit_ns) && wait_tile(0);
         if (ok) {
           fence_after();
           for (int h = 0; h < halves; ++h) scores(h, 0);
-          commit(smem_addr(&sm.kv_empty[0]));
+          commit(smem_addr(&sm.kv_empty[0]), lead);
         }
       }
       for (int j = 0; j < n_steps && ok; ++j) {
@@ -724,19 +736,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool more = j + 1 < n_steps;
         for (int h = 0; h < halves && ok; ++h) {
           if ((h == 0 && !wait_tile(nv)) ||
-              !bar_wait(smem_addr(&sm.p_half[h]), j & 1, gave_up, a.wait_limit_ns)) {
+              !warp_wait(smem_addr(&sm.p_half[h]), j & 1, gave_up, a.wait_limit_ns)) {
             ok = false;
             break;
           }
           fence_after();
           output(h, nv, 0, j == 0);
-          if (!bar_wait(smem_addr(&sm.p_full[h]), j & 1, gave_up, a.wait_limit_ns)) {
+          if (!warp_wait(smem_addr(&sm.p_full[h]), j & 1, gave_up, a.wait_limit_ns)) {
             ok = false;
             break;
           }
           fence_after();
           output(h, nv, 1, false);
-          if (h == halves - 1) commit(smem_addr(&sm.kv_empty[nv % kSlots]));
+          if (h == halves - 1) commit(smem_addr(&sm.kv_empty[nv % kSlots]), lead);
           if (more) {
             if (h == 0 && !wait_tile(nk)) {
               ok = false;
@@ -744,18 +756,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             fence_after();
             scores(h, nk);
-            if (h == halves - 1) commit(smem_addr(&sm.kv_empty[nk % kSlots]));
+            if (h == halves - 1) commit(smem_addr(&sm.kv_empty[nk % kSlots]), lead);
           } else {
-            commit(smem_addr(&sm.o_full[h]));
+            commit(smem_addr(&sm.o_full[h]), lead);
           }
         }
       }
       if (!ok) {
         *gave_up = 1;
-        atomicOr(a.err, kDevErrTimeout);
+        if (lane == 0) atomicOr(a.err, kDevErrTimeout);
       }
       // no MMA may still run when the tensor memory is freed
-      commit(smem_addr(&sm.mma_done));
+      commit(smem_addr(&sm.mma_done), lead);
       bar_wait(smem_addr(&sm.mma_done), 0, nullptr, 2000000000ull);
     }
   }
