@@ -4,13 +4,24 @@ Torch-facing helpers of nvfp4_rope, nvfp4_kv8_write, nvfp4_kv8_read and
 nvfp4_kv8_attention (include/nvfp4.h): they check shapes and types, allocate
 outputs and marshal pointers and streams.  Work goes to the current stream of
 the tensors' device, or to ``stream``.
+
+These calls are made once per layer and token, so the host side is kept short:
+the C structs are packed with ``struct`` (the formats below) instead of being
+built field by field.
 """
 from __future__ import annotations
 
 import math
+import struct
 from dataclasses import dataclass
 
-from . import _dtype_code, _torch, capi, workspace
+from . import NVFP4_BF16, NVFP4_F32, _torch, capi, workspace
+
+_ROPE_TENSOR = "PPqqqqq"                        # nvfp4_rope_tensor
+_ROPE_PARAMS = struct.Struct("@5id3i4x")        # nvfp4_rope_params
+_BATCH = struct.Struct("@Pqi4xPPi4xqi4x")       # nvfp4_kv8_batch
+_QUERY = struct.Struct("@PPPi4xqqqqfiii")       # nvfp4_kv8_query
+_ROPE_TENSORS = [struct.Struct("@" + _ROPE_TENSOR * n) for n in range(9)]
 
 
 @dataclass
@@ -35,13 +46,11 @@ class KV8Cache:
                 raise ValueError("scales are contiguous fp32 [pages, heads] tensors")
         if any(t.device != k.device for t in (self.v_codes, self.k_scales, self.v_scales)):
             raise ValueError("a cache lives on one device")
-        self.desc = capi.nvfp4_kv8_cache(k.data_ptr(), self.v_codes.data_ptr(),
-                                         self.k_scales.data_ptr(), self.v_scales.data_ptr(),
-                                         k.shape[0], k.shape[1], k.shape[2], k.shape[3])
-
-    @property
-    def page_tokens(self):
-        return self.k_codes.shape[2]
+        self.heads, self.page_tokens, self.head_dim = k.shape[1:]
+        self.device, self.index = k.device, k.get_device()
+        self.desc = bytes(capi.nvfp4_kv8_cache(
+            k.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
+            self.v_scales.data_ptr(), *k.shape))
 
 
 def kv8_cache(pages, heads, page_tokens=64, head_dim=128, device=None):
@@ -58,40 +67,62 @@ def kv8_cache(pages, heads, page_tokens=64, head_dim=128, device=None):
     return KV8Cache(codes(), codes(), scales(), scales())
 
 
-def _launch(device, stream, call):
-    """call(stream handle) with `device` current."""
+def _type(t):
     torch = _torch()
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if device.index in (None, torch.cuda.current_device()):
-        return call(s.cuda_stream)
-    with torch.cuda.device(device):
-        return call(s.cuda_stream)
+    if t.dtype is torch.bfloat16:
+        return NVFP4_BF16
+    if t.dtype is torch.float32:
+        return NVFP4_F32
+    raise TypeError("unsupported dtype %s" % t.dtype)
 
 
-def _packed(x, heads, dim, what):
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
-        raise ValueError("%s is [rows, %d, %d], not %s" % (what, heads, dim, tuple(x.shape)))
-    if x.stride(2) != 1:
+def _call(name, index, stream, *args):
+    """Calls the library with `stream`, or device `index`'s current stream, as
+    the last argument and with that device current."""
+    if index < 0:
+        raise ValueError("%s works on CUDA tensors" % name)
+    torch = _torch()
+    fn = getattr(capi.load(), name)
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, handle)
+    if st:
+        raise capi.NVFP4Error(name, st)
+
+
+def _packed(x, rows, cache, what):
+    """Strides of a [rows, heads, head_dim] tensor of the cache's device."""
+    if x.dim() != 3 or x.shape[0] != rows or x.shape[2] != cache.head_dim:
+        raise ValueError("%s is [%d, heads, %d], not %s" % (what, rows, cache.head_dim,
+                                                            tuple(x.shape)))
+    if x.get_device() != cache.index:
+        raise ValueError("%s is not on the cache's device" % what)
+    t, h, e = x.stride()
+    if e != 1:
         raise ValueError("%s: the elements of a head are not contiguous" % what)
-    return x
+    return t, h
 
 
 def _batch(cache, page_table, lens, starts, rows, max_rows):
-    torch = _torch()
-    i32, dev = torch.int32, cache.k_codes.device
-    if page_table.dtype != i32 or lens.dtype != i32 or starts.dtype != i32:
+    i32 = _torch().int32
+    if not (page_table.dtype is i32 and lens.dtype is i32 and starts.dtype is i32):
         raise TypeError("page_table, lens and starts are int32 tensors")
-    if page_table.device != dev or lens.device != dev or starts.device != dev:
+    at = cache.index
+    if page_table.get_device() != at or lens.get_device() != at or starts.get_device() != at:
         raise ValueError("page_table, lens and starts are on the cache's device")
-    n = lens.shape[0]
-    if page_table.dim() != 2 or page_table.shape[0] != n or starts.shape != (n + 1,):
+    n = lens.numel()
+    if page_table.dim() != 2 or lens.dim() != 1 or starts.dim() != 1 or (
+            page_table.shape[0] != n or starts.numel() != n + 1):
         raise ValueError("page_table is [n, pages], lens [n], starts [n + 1]")
-    if page_table.stride(1) != 1 and page_table.shape[1] > 1 or not (
-            lens.is_contiguous() and starts.is_contiguous()):
+    stride, one = page_table.stride()
+    width = page_table.shape[1]
+    if (one != 1 and width > 1) or not lens.is_contiguous() or not starts.is_contiguous():
         raise ValueError("page_table's rows, lens and starts are contiguous")
-    return capi.nvfp4_kv8_batch(page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]),
-                                page_table.shape[1], lens.data_ptr(), starts.data_ptr(), n, rows,
-                                rows if max_rows is None else max_rows)
+    return _BATCH.pack(page_table.data_ptr(), stride if stride > width else width, width,
+                       lens.data_ptr(), starts.data_ptr(), n, rows, max_rows)
 
 
 def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True, inverse=False,
@@ -100,35 +131,39 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     type, strided) turned by positions (int32 [tokens, axes]).  With ``inverse``
     the gradients of xs from those of the outputs.  outs may be xs (in place)."""
     torch = _torch()
-    n = len(xs)
-    axes = len(sections)
-    if n < 1 or not 1 <= axes <= 4:
-        raise ValueError("rope takes at least one tensor and 1 to 4 sections")
-    tokens, _, dim = xs[0].shape
-    if positions.dtype != torch.int32 or positions.dim() != 2 or positions.shape[0] != tokens or (
-            positions.shape[1] < axes):
-        raise ValueError("positions is int32 [tokens, axes]")
-    if positions.stride(1) != 1 and positions.shape[1] > 1:
-        raise ValueError("positions' rows are contiguous")
+    n, axes = len(xs), len(sections)
+    if not 1 <= n <= 8 or not 1 <= axes <= 4:
+        raise ValueError("rope takes 1 to 8 tensors and 1 to 4 sections")
     if outs is None:
-        outs = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in xs]
-    descs = (capi.nvfp4_rope_tensor * n)()
-    for i, (x, o) in enumerate(zip(xs, outs)):
-        if x.dim() != 3 or x.shape[0] != tokens or x.shape[2] != dim or o.shape != x.shape:
+        outs = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs]
+    first = xs[0]
+    if first.dim() != 3:
+        raise ValueError("rope's tensors are [tokens, heads, head_dim]")
+    tokens, _, dim = first.shape
+    at, kind = positions.get_device(), first.dtype
+    if positions.dtype is not torch.int32 or positions.dim() != 2 or (
+            positions.shape[0] != tokens or positions.shape[1] < axes):
+        raise ValueError("positions is int32 [tokens, axes]")
+    stride, one = positions.stride()
+    if one != 1 and positions.shape[1] > 1:
+        raise ValueError("positions' rows are contiguous")
+    fields = []
+    for x, o in zip(xs, outs):
+        if x.dim() != 3 or o.shape != x.shape or x.shape[0] != tokens or x.shape[2] != dim:
             raise ValueError("rope's tensors are [tokens, heads, head_dim] of one token count")
-        if x.dtype != xs[0].dtype or o.dtype != x.dtype or x.device != positions.device:
+        if x.dtype is not kind or o.dtype is not kind or x.get_device() != at or (
+                o.get_device() != at):
             raise ValueError("rope's tensors are of one type and device")
         xt, xh, xe = x.stride()
         ot, oh, oe = o.stride()
-        if xe != 1 or oe != 1:
+        if (xe != 1 or oe != 1) and dim > 1:
             raise ValueError("rope: the elements of a head are not contiguous")
-        descs[i] = capi.nvfp4_rope_tensor(x.data_ptr(), o.data_ptr(), x.shape[1], xt, xh, ot, oh)
-    rp = capi.nvfp4_rope_params(axes, tuple(sections), theta, bool(interleaved), bool(per_axis),
-                                bool(inverse))
-    st = _launch(positions.device, stream, lambda s: capi.nvfp4_rope(
-        descs, n, _dtype_code(xs[0]), tokens, dim, positions.data_ptr(),
-        max(positions.stride(0), positions.shape[1]), rp, s))
-    capi.check("nvfp4_rope", st)
+        fields += (x.data_ptr(), o.data_ptr(), x.shape[1], xt, xh, ot, oh)
+    pad = (0, 0, 0, 0)
+    rp = _ROPE_PARAMS.pack(axes, *sections, *pad[axes:], theta, bool(interleaved), bool(per_axis),
+                           bool(inverse))
+    _call("nvfp4_rope", at, stream, _ROPE_TENSORS[n].pack(*fields), n, _type(first), tokens, dim,
+          positions.data_ptr(), stride if stride > axes else axes, rp)
     return outs
 
 
@@ -136,19 +171,15 @@ def kv8_write(cache, k, v, page_table, lens, starts, max_new=None, ws=None, stre
     """One nvfp4_kv8_write call: rows starts[s]..starts[s+1] of k and v ([rows,
     heads, head_dim]) become sequence s's tokens from lens[s] on.  max_new: at
     least the most rows of a sequence (default: all rows)."""
-    _, heads, _, dim = cache.k_codes.shape
-    _packed(k, heads, dim, "k")
-    _packed(v, heads, dim, "v")
-    if v.shape[0] != k.shape[0] or v.dtype != k.dtype:
-        raise ValueError("k and v have the same rows and type")
-    if k.device != cache.k_codes.device or v.device != k.device:
-        raise ValueError("k and v are on the cache's device")
-    ws = workspace(0, k.device) if ws is None else ws
-    b = _batch(cache, page_table, lens, starts, k.shape[0], max_new)
-    st = _launch(k.device, stream, lambda s: capi.nvfp4_kv8_write(
-        cache.desc, b, _dtype_code(k), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-        v.stride(0), v.stride(1), ws.data_ptr(), ws.numel(), s))
-    capi.check("nvfp4_kv8_write", st)
+    rows = k.shape[0]
+    kt, kh = _packed(k, rows, cache, "k")
+    vt, vh = _packed(v, rows, cache, "v")
+    if k.shape[1] != cache.heads or v.shape[1] != cache.heads or v.dtype is not k.dtype:
+        raise ValueError("k and v have the cache's heads and one type")
+    b = _batch(cache, page_table, lens, starts, rows, rows if max_new is None else max_new)
+    ws = workspace(0, cache.device) if ws is None else ws
+    _call("nvfp4_kv8_write", cache.index, stream, cache.desc, b, _type(k), k.data_ptr(), kt, kh,
+          v.data_ptr(), vt, vh, ws.data_ptr(), ws.numel())
 
 
 def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype=None, outs=None,
@@ -156,24 +187,19 @@ def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype
     """One nvfp4_kv8_read call: sequence s's tokens from begins[s] on become rows
     starts[s]..starts[s+1] of the returned (k, v), [rows, heads, head_dim]."""
     torch = _torch()
-    _, heads, _, dim = cache.k_codes.shape
-    dev = cache.k_codes.device
     if outs is None:
-        out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-        outs = tuple(torch.empty((rows, heads, dim), dtype=out_dtype, device=dev) for _ in "kv")
+        out = torch.empty((2, rows, cache.heads, cache.head_dim), device=cache.device,
+                          dtype=torch.bfloat16 if out_dtype is None else out_dtype)
+        outs = out[0], out[1]
     k, v = outs
-    _packed(k, heads, dim, "k")
-    _packed(v, heads, dim, "v")
-    if k.shape[0] != rows or v.shape[0] != rows or v.dtype != k.dtype:
-        raise ValueError("the outputs have `rows` rows and one type")
-    if k.device != dev or v.device != dev:
-        raise ValueError("the outputs are on the cache's device")
-    ws = workspace(0, dev) if ws is None else ws
-    b = _batch(cache, page_table, begins, starts, rows, max_tokens)
-    st = _launch(dev, stream, lambda s: capi.nvfp4_kv8_read(
-        cache.desc, b, _dtype_code(k), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(),
-        v.stride(0), v.stride(1), ws.data_ptr(), ws.numel(), s))
-    capi.check("nvfp4_kv8_read", st)
+    kt, kh = _packed(k, rows, cache, "k")
+    vt, vh = _packed(v, rows, cache, "v")
+    if k.shape[1] != cache.heads or v.shape[1] != cache.heads or v.dtype is not k.dtype:
+        raise ValueError("k and v have the cache's heads and one type")
+    b = _batch(cache, page_table, begins, starts, rows, rows if max_tokens is None else max_tokens)
+    ws = workspace(0, cache.device) if ws is None else ws
+    _call("nvfp4_kv8_read", cache.index, stream, cache.desc, b, _type(k), k.data_ptr(), kt, kh,
+          v.data_ptr(), vt, vh, ws.data_ptr(), ws.numel())
     return outs
 
 
@@ -181,10 +207,9 @@ def kv8_attention_workspace(cache, page_table, starts, q_heads, max_q):
     """Workspace for kv8_attention of these sizes, error word zeroed (the rest
     needs no initialization).  Serves one call in flight at a time."""
     torch = _torch()
-    _, heads, page_tokens, dim = cache.k_codes.shape
     ws = torch.empty(capi.nvfp4_kv8_attention_workspace_bytes(
-        heads, dim, page_tokens, q_heads, starts.shape[0] - 1, max_q, page_table.shape[1]),
-        dtype=torch.uint8, device=cache.k_codes.device)
+        cache.heads, cache.head_dim, cache.page_tokens, q_heads, starts.numel() - 1, max_q,
+        page_table.shape[1]), dtype=torch.uint8, device=cache.device)
     ws[:capi.nvfp4_workspace_bytes(0)].zero_()
     return ws
 
@@ -196,31 +221,33 @@ def kv8_attention(q, cache, page_table, lens, starts, max_q=None, scale=None, ca
     max_q: at least the most queries of a sequence (default: all rows).  lse: an
     fp32 [rows, q_heads] tensor that receives the log-sum-exps."""
     torch = _torch()
-    _, heads, page_tokens, dim = cache.k_codes.shape
-    rows, q_heads = q.shape[0], q.shape[1]
-    _packed(q, q_heads, dim, "q")
-    if out is None:
-        out = torch.empty((rows, q_heads, dim), dtype=q.dtype, device=q.device)
-    _packed(out, q_heads, dim, "out")
-    if q.dtype != torch.bfloat16 or out.dtype != q.dtype:
+    if q.dtype is not torch.bfloat16:
         raise TypeError("q and out are bfloat16")
-    if out.shape[0] != rows:
-        raise ValueError("out has q's rows")
-    dev = cache.k_codes.device
-    if q.device != dev or out.device != dev or (lse is not None and lse.device != dev):
-        raise ValueError("q, out and lse are on the cache's device")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, q_heads)
-                            or not lse.is_contiguous()):
-        raise ValueError("lse is contiguous fp32 [rows, q_heads]")
+    rows = q.shape[0]
+    qt, qh = _packed(q, rows, cache, "q")
+    q_heads = q.shape[1]
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    elif out.dtype is not torch.bfloat16:
+        raise TypeError("q and out are bfloat16")
+    ot, oh = _packed(out, rows, cache, "out")
+    if out.shape[1] != q_heads:
+        raise ValueError("out has q's heads")
+    at = 0
+    if lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != (rows, q_heads) or (
+                not lse.is_contiguous() or lse.get_device() != cache.index):
+            raise ValueError("lse is contiguous fp32 [rows, q_heads] on the cache's device")
+        at = lse.data_ptr()
+    if max_q is None:
+        max_q = rows
     b = _batch(cache, page_table, lens, starts, rows, max_q)
     if ws is None:
-        ws = kv8_attention_workspace(cache, page_table, starts, q_heads, b.max_rows)
-    query = capi.nvfp4_kv8_query(q.data_ptr(), out.data_ptr(),
-                                 None if lse is None else lse.data_ptr(), q_heads, q.stride(0),
-                                 q.stride(1), out.stride(0), out.stride(1),
-                                 1.0 / math.sqrt(dim) if scale is None else scale, bool(causal),
-                                 window, sink)
-    st = _launch(dev, stream, lambda s: capi.nvfp4_kv8_attention(
-        cache.desc, b, query, ws.data_ptr(), ws.numel(), s))
-    capi.check("nvfp4_kv8_attention", st)
+        ws = kv8_attention_workspace(cache, page_table, starts, q_heads, max_q)
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.head_dim)
+    query = _QUERY.pack(q.data_ptr(), out.data_ptr(), at, q_heads, qt, qh, ot, oh, scale,
+                        bool(causal), window, sink)
+    _call("nvfp4_kv8_attention", cache.index, stream, cache.desc, b, query, ws.data_ptr(),
+          ws.numel())
     return out

@@ -90,9 +90,6 @@ _V, _I32, _I64, _U32, _SZ = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ct
                              ctypes.c_size_t)
 _QP = ctypes.POINTER(nvfp4_qparams)
 _TD = ctypes.POINTER(nvfp4_tensor_desc)
-_RT, _RP = ctypes.POINTER(nvfp4_rope_tensor), ctypes.POINTER(nvfp4_rope_params)
-_KC, _KB = ctypes.POINTER(nvfp4_kv8_cache), ctypes.POINTER(nvfp4_kv8_batch)
-_KQ = ctypes.POINTER(nvfp4_kv8_query)
 
 _SIGS = {
     "nvfp4_workspace_bytes": (_SZ, [_I32]),
@@ -121,10 +118,10 @@ _SIGS = {
     "nvfp4_gemm_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I32]),
     "nvfp4_gemm_lora": (_I32, [_V, _V, _V, _V, _V, _V, _I64, _I64, _I64, _V, _I64, _V, _I64, _I64,
                                ctypes.c_float, _V, _SZ, _V, _I32, _I64, _I32, _V, _SZ, _V]),
-    "nvfp4_rope": (_I32, [_RT, _I32, _I32, _I64, _I32, _V, _I64, _RP, _V]),
-    "nvfp4_kv8_write": (_I32, [_KC, _KB, _I32, _V, _I64, _I64, _V, _I64, _I64, _V, _SZ, _V]),
-    "nvfp4_kv8_read": (_I32, [_KC, _KB, _I32, _V, _I64, _I64, _V, _I64, _I64, _V, _SZ, _V]),
-    "nvfp4_kv8_attention": (_I32, [_KC, _KB, _KQ, _V, _SZ, _V]),
+    "nvfp4_rope": (_I32, [_V, _I32, _I32, _I64, _I32, _V, _I64, _V, _V]),
+    "nvfp4_kv8_write": (_I32, [_V, _V, _I32, _V, _I64, _I64, _V, _I64, _I64, _V, _SZ, _V]),
+    "nvfp4_kv8_read": (_I32, [_V, _V, _I32, _V, _I64, _I64, _V, _I64, _I64, _V, _SZ, _V]),
+    "nvfp4_kv8_attention": (_I32, [_V, _V, _V, _V, _SZ, _V]),
     "nvfp4_kv8_attention_workspace_bytes": (_SZ, [_I32, _I32, _I32, _I32, _I32, _I32, _I32]),
 }
 
@@ -255,26 +252,31 @@ def nvfp4_set_test_stall(on):
     return _call("nvfp4_set_test_stall", on)
 
 
+def _at(x):
+    """Address of a struct given as a ctypes Structure or as its packed bytes."""
+    return x if isinstance(x, bytes) else ctypes.byref(x)
+
+
 def nvfp4_rope(tensors, n, dtype, tokens, head_dim, positions, positions_stride, rp, stream):
     return _call("nvfp4_rope", tensors, n, dtype, tokens, head_dim, positions, positions_stride,
-                 ctypes.byref(rp), stream)
+                 _at(rp), stream)
 
 
 def nvfp4_kv8_write(cache, batch, dtype, k, k_token, k_head, v, v_token, v_head, ws, ws_bytes,
                     stream):
-    return _call("nvfp4_kv8_write", ctypes.byref(cache), ctypes.byref(batch), dtype, k, k_token,
+    return _call("nvfp4_kv8_write", _at(cache), _at(batch), dtype, k, k_token,
                  k_head, v, v_token, v_head, ws, ws_bytes, stream)
 
 
 def nvfp4_kv8_read(cache, batch, dtype, k, k_token, k_head, v, v_token, v_head, ws, ws_bytes,
                    stream):
-    return _call("nvfp4_kv8_read", ctypes.byref(cache), ctypes.byref(batch), dtype, k, k_token,
+    return _call("nvfp4_kv8_read", _at(cache), _at(batch), dtype, k, k_token,
                  k_head, v, v_token, v_head, ws, ws_bytes, stream)
 
 
 def nvfp4_kv8_attention(cache, batch, query, ws, ws_bytes, stream):
-    return _call("nvfp4_kv8_attention", ctypes.byref(cache), ctypes.byref(batch),
-                 ctypes.byref(query), ws, ws_bytes, stream)
+    return _call("nvfp4_kv8_attention", _at(cache), _at(batch),
+                 _at(query), ws, ws_bytes, stream)
 
 
 def nvfp4_kv8_attention_workspace_bytes(heads, head_dim, page_tokens, q_heads, n, max_rows,

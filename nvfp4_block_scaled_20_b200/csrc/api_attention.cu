@@ -73,6 +73,9 @@ nvfp4_status write_or_read(bool write, const nvfp4_kv8_cache* cache, const nvfp4
     if (!aligned(strides[i] * elem_bytes(dtype), 16)) return NVFP4_ERR_ALIGN;
   }
   if (!ws || ws_bytes < nvfp4_workspace_bytes(0)) return NVFP4_ERR_WORKSPACE;
+  // one CTA per page that a sequence may touch, head, K and V: a grid dimension
+  if (((int64_t)batch->max_rows / cache->page_tokens + 2) * cache->heads * 2 > INT32_MAX)
+    return NVFP4_ERR_SHAPE;
   const Kv8Rows r{{k, v}, {strides[0], strides[2]}, {strides[1], strides[3]}};
   uint32_t* err = static_cast<uint32_t*>(ws);
   const bool bf16 = dtype == NVFP4_BF16;
@@ -96,7 +99,6 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n, int32_t dty
     return NVFP4_ERR_SHAPE;
   RopeArgs a;
   a.n = 0;
-  a.heads = 0;
   a.tokens = tokens;
   a.dim = head_dim;
   a.pos = positions;
@@ -120,9 +122,8 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n, int32_t dty
       if (s % 2) return NVFP4_ERR_ALIGN;  // pairs of elements
     }
     if (!aligned(t.x, 2 * eb) || !aligned(t.out, 2 * eb)) return NVFP4_ERR_ALIGN;
-    a.heads += (int32_t)t.heads;
     a.t[a.n++] = RopeTensor{t.x, t.out, t.x_token_stride, t.x_head_stride, t.out_token_stride,
-                            t.out_head_stride, a.heads};
+                            t.out_head_stride, (int32_t)t.heads, 0, 0, 0};
   }
   if (tokens == 0 || a.n == 0) return NVFP4_OK;
   if (!positions) return NVFP4_ERR_INVALID_ARG;

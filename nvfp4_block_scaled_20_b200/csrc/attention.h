@@ -17,13 +17,14 @@ struct RopeTensor {
   const void* x;
   void* out;
   int64_t x_token, x_head, out_token, out_head;  // strides in elements
-  int32_t head_end;                              // heads of this and the earlier tensors
+  int32_t heads;
+  // filled by the launch: a thread's step in tokens and heads, 65536 / heads + 1
+  int32_t step_tokens, step_heads, heads_inv;
 };
 
 struct RopeArgs {
   RopeTensor t[kMaxRopeTensors];
   int32_t n;
-  int32_t heads;  // of all tensors
   int64_t tokens;
   int32_t dim;         // head_dim
   int32_t pairs;       // rotated pairs, the rest of a head is copied
@@ -32,7 +33,7 @@ struct RopeArgs {
   double turns[kMaxRopePairs];   // turns per position of pair i, signed by the direction
   uint8_t axis[kMaxRopePairs];
 };
-cudaError_t launch_rope(const RopeArgs& a, bool bf16, bool interleaved, cudaStream_t s);
+cudaError_t launch_rope(RopeArgs& a, bool bf16, bool interleaved, cudaStream_t s);
 
 // --------------------------------------------------------------- kv cache
 constexpr int kKv8MinExp = -40, kKv8MaxExp = 40;  // exponents of the cache's scales

@@ -18,8 +18,12 @@
 // What bounds both: bytes.  Write reads 2 B (bf16) and writes 1 B per value,
 // read the reverse.  One CTA owns the (page, head, K or V) block, so a page's
 // maximum, its scale and its codes need one pass over the data held in
-// registers (64 values per thread), no atomics and no second launch; the
-// result does not depend on the order of CTAs.
+// registers (64 values per thread, as they were loaded), no atomics and no
+// second launch; the result does not depend on the order of CTAs.  A token's
+// heads lie next to each other in memory, so neighbouring CTAs take
+// neighbouring heads of a page's tokens, and K's CTA has V's beside it.
+#include <climits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -61,22 +65,38 @@ __device__ __forceinline__ uint32_t finite_abs_bits(float v) {
   return a < 0x7F800000u ? a : 0u;
 }
 
-// 8 consecutive values of a packed row.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float v[8]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+// 8 consecutive values of a packed row, as loaded and as fp32.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    a = __ldg(reinterpret_cast<const uint4*>(p));
   }
-}
-__device__ __forceinline__ void load8(const float* p, float v[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
+  __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void values(float v[8]) const {
+    const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldg(reinterpret_cast<const float4*>(p));
+    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ void values(float v[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
 
 // Four fp32 values -> four E4M3 codes (round to nearest even, saturating).
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -105,41 +125,44 @@ __global__ void __launch_bounds__(kTokens * kDim / 64)
   constexpr int kThreads = kTokens * kDim / 64;
   constexpr int kCols = kDim / 8, kRows = kThreads / kCols, kSteps = 8;
   static_assert(kRows * kSteps == kTokens, "each thread holds 64 values");
-  const int which = blockIdx.y & 1, head = blockIdx.y >> 1, s = blockIdx.z;
+  const int blocks = 2 * c.heads;  // of a page: K and V of each head
+  const int slot0 = blockIdx.x / blocks, in_page = blockIdx.x - slot0 * blocks;
+  const int which = in_page & 1, head = in_page >> 1, s = blockIdx.y;
   Seq q;
   if (!load_seq(b, kTokens, s, q)) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(err, kDevErrShape);
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err, kDevErrShape);
     return;
   }
-  const int64_t slot = q.len / kTokens + blockIdx.x;  // of the sequence's pages
+  const int64_t slot = q.len / kTokens + slot0;  // of the sequence's pages
   const int64_t base = slot * kTokens;
   if (q.n == 0 || base >= q.len + q.n) return;
-  const int64_t page = b.table[s * b.table_stride + slot];
-  if (page < 0 || page >= c.pages) {
-    if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(err, kDevErrShape);
-    return;
-  }
+  const int64_t page = b.table[s * b.table_stride + slot];  // checked below
   // rows [r0, r1) of the page are new; its rows before r0 hold earlier tokens
   const int r0 = (int)(q.len > base ? q.len - base : 0);
   const int r1 = (int)(q.len + q.n - base < kTokens ? q.len + q.n - base : kTokens);
   const int col = (threadIdx.x % kCols) * 8, row = threadIdx.x / kCols;
   const T* x = static_cast<const T*>(r.x[which]) + head * r.head[which] + col;
-  float v[kSteps][8];
+  Raw8<T> v[kSteps];
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
     const int at = row + k * kRows;
-    if (at >= r0 && at < r1) {
-      load8(x + (q.first + (base + at - q.len)) * r.token[which], v[k]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
-    }
+    if (at >= r0 && at < r1)
+      v[k].load(x + (q.first + (base + at - q.len)) * r.token[which]);
+    else
+      v[k].zero();
+  }
+  if (page < 0 || page >= c.pages) {
+    if (in_page == 0 && threadIdx.x == 0) atomicOr(err, kDevErrShape);
+    return;
   }
   uint32_t m = 0;
 #pragma unroll
-  for (int k = 0; k < kSteps; ++k)
+  for (int k = 0; k < kSteps; ++k) {
+    float f[8];
+    v[k].values(f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(v[k][i]));
+    for (int i = 0; i < 8; ++i) m = max(m, finite_abs_bits(f[i]));
+  }
   m = __reduce_max_sync(0xFFFFFFFFu, m);
   if constexpr (kThreads > 32) {
     __shared__ uint32_t warp_max[kThreads / 32];
@@ -182,12 +205,25 @@ __global__ void __launch_bounds__(kTokens * kDim / 64)
     const int at = row + k * kRows;
     if (at < r0 || at >= r1) continue;
     float f[8];
+    v[k].values(f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = v[k][i] * inv;
+    for (int i = 0; i < 8; ++i) f[i] *= inv;
     *reinterpret_cast<uint2*>(codes + at * kDim) =
         make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
   }
   if (threadIdx.x == 0) c.scales[which][block] = scale;
+}
+
+// 32 bytes, one store where the row is 32-byte aligned (whole sectors).
+__device__ __forceinline__ void store32(uint8_t* p, const uint32_t h[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(h[0]),
+                 "r"(h[1]), "r"(h[2]), "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  }
 }
 
 // One CTA per (page of the sequence, head, K or V): 16 codes per thread step.
@@ -198,23 +234,25 @@ __global__ void __launch_bounds__(kTokens * kDim / 64)
   constexpr int kThreads = kTokens * kDim / 64;
   constexpr int kCols = kDim / 16, kRows = kThreads / kCols, kSteps = 4;
   static_assert(kRows * kSteps == kTokens, "each thread holds 64 values");
-  const int which = blockIdx.y & 1, head = blockIdx.y >> 1, s = blockIdx.z;
+  const int blocks = 2 * c.heads;  // of a page: K and V of each head
+  const int slot0 = blockIdx.x / blocks, in_page = blockIdx.x - slot0 * blocks;
+  const int which = in_page & 1, head = in_page >> 1, s = blockIdx.y;
   Seq q;
   if (!load_seq(b, kTokens, s, q)) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(err, kDevErrShape);
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err, kDevErrShape);
     return;
   }
-  const int64_t slot = q.len / kTokens + blockIdx.x;
+  const int64_t slot = q.len / kTokens + slot0;
   const int64_t base = slot * kTokens;
   if (q.n == 0 || base >= q.len + q.n) return;
-  const int64_t page = b.table[s * b.table_stride + slot];
-  if (page < 0 || page >= c.pages) {
-    if (blockIdx.y == 0 && threadIdx.x == 0) atomicOr(err, kDevErrShape);
-    return;
-  }
+  const int64_t page = b.table[s * b.table_stride + slot];  // checked below
   const int r0 = (int)(q.len > base ? q.len - base : 0);
   const int r1 = (int)(q.len + q.n - base < kTokens ? q.len + q.n - base : kTokens);
   const int col = (threadIdx.x % kCols) * 16, row = threadIdx.x / kCols;
+  if (page < 0 || page >= c.pages) {
+    if (in_page == 0 && threadIdx.x == 0) atomicOr(err, kDevErrShape);
+    return;
+  }
   const int64_t block = page * c.heads + head;
   const uint8_t* codes = c.codes[which] + block * (int64_t)(kTokens * kDim) + col;
   const float scale = c.scales[which][block];
@@ -225,6 +263,9 @@ __global__ void __launch_bounds__(kTokens * kDim / 64)
     if (at >= r0 && at < r1) w[k] = __ldg(reinterpret_cast<const uint4*>(codes + at * kDim));
   }
   T* out = static_cast<T*>(r.x[which]) + head * r.head[which] + col;
+  const bool wide =
+      (((uintptr_t)r.x[which] | (uintptr_t)(r.head[which] * sizeof(T)) |
+        (uintptr_t)(r.token[which] * sizeof(T))) & 31) == 0;
 #pragma unroll
   for (int k = 0; k < kSteps; ++k) {
     const int at = row + k * kRows;
@@ -232,24 +273,23 @@ __global__ void __launch_bounds__(kTokens * kDim / 64)
     T* o = out + (q.first + (base + at - q.len)) * r.token[which];
     const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      float f[8];
-      e4m3x4_values(u[i], f);
-      e4m3x4_values(u[i + 1], f + 4);
+    for (int i = 0; i < 4; i += 4 / (int)sizeof(T) * 2) {
+      // 32 bytes of output: 16 values of bf16, 8 of fp32
+      constexpr int kOut = 32 / (int)sizeof(T);
+      float f[kOut];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] *= scale;
-      if constexpr (sizeof(T) == 2) {
-        uint32_t h[4];
+      for (int j = 0; j < kOut / 4; ++j) e4m3x4_values(u[i + j], f + 4 * j);
+      uint32_t h[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(T) == 2) {
+          const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * j] * scale, f[2 * j + 1] * scale);
           h[j] = *reinterpret_cast<const uint32_t*>(&p);
+        } else {
+          h[j] = __float_as_uint(f[j] * scale);
         }
-        reinterpret_cast<uint4*>(o)[i / 2] = make_uint4(h[0], h[1], h[2], h[3]);
-      } else {
-        reinterpret_cast<float4*>(o)[i] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(o)[i + 1] = make_float4(f[4], f[5], f[6], f[7]);
       }
+      store32(reinterpret_cast<uint8_t*>(o) + (i / (4 / (int)sizeof(T) * 2)) * 32, h, wide);
     }
   }
 }
@@ -258,8 +298,9 @@ template <typename T, int kDim, int kTokens>
 cudaError_t launch(bool write, const Kv8Cache& c, const Kv8Batch& b, const Kv8Rows& r,
                    uint32_t* err, cudaStream_t s) {
   // a sequence's rows touch at most this many pages
-  const unsigned slots = (unsigned)((b.max_rows - 1 + kTokens - 1) / kTokens + 1);
-  const dim3 grid(slots, (unsigned)c.heads * 2, (unsigned)b.n);
+  const int64_t slots = ((int64_t)b.max_rows - 1 + kTokens - 1) / kTokens + 1;
+  if (slots * c.heads * 2 > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const dim3 grid((unsigned)(slots * c.heads * 2), (unsigned)b.n);
   constexpr int kThreads = kTokens * kDim / 64;
   if (write)
     kv8_write_kernel<T, kDim, kTokens><<<grid, kThreads, 0, s>>>(c, b, r, err);

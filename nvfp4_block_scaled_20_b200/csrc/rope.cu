@@ -8,8 +8,9 @@
 // What bounds it: every element is read and written once, 4 B of bf16 against
 // three operations.  The angles belong to a token, not to its heads, so a CTA
 // computes the sine and cosine of its tokens' pairs once into shared memory --
-// one of each per thread -- and its threads then stream the heads of all
-// tensors past them with 16-byte loads, four heads in flight per thread.
+// one of each per thread -- and its threads then stream the heads of one
+// tensor past them with 16-byte loads, several heads in flight per thread; the
+// first ones are on the way while the angles are computed.
 //
 // The angle in turns is a double product: position * rate reaches 10^4..10^5
 // turns, where fp32 would keep 2^-8 of a turn.  Its fraction, exact, is
@@ -24,18 +25,24 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
-  return __float2bfloat16_rn(v);
+// Elements 2 i, 2 i + 1 of a vector as fp32, and back (rounded once).
+__device__ __forceinline__ float2 pair_of(const __nv_bfloat16* v) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(v);
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
-template <>
-__device__ __forceinline__ float from_f32<float>(float v) {
-  return v;
+__device__ __forceinline__ float2 pair_of(const float* v) { return make_float2(v[0], v[1]); }
+__device__ __forceinline__ void set_pair(__nv_bfloat16* v, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(v) = __floats2bfloat162_rn(a, b);
 }
+__device__ __forceinline__ void set_pair(float* v, float a, float b) { v[0] = a, v[1] = b; }
+__device__ __forceinline__ float one_of(const __nv_bfloat16* v) { return __bfloat162float(*v); }
+__device__ __forceinline__ float one_of(const float* v) { return *v; }
+__device__ __forceinline__ void set_one(__nv_bfloat16* v, float a) { *v = __float2bfloat16_rn(a); }
+__device__ __forceinline__ void set_one(float* v, float a) { *v = a; }
+
+// x / d for x < 256 and 1 <= d <= 256, inv = 65536 / d + 1: the product is off
+// by x d / 65536 < 1 of a unit.
+__device__ __forceinline__ int div256(int x, int inv) { return (x * inv) >> 16; }
 
 template <typename T, int N>
 struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Vec {
@@ -45,96 +52,128 @@ struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Vec {
 // P pairs per thread step.  Interleaved: elements [2i, 2i + 2P), one vector;
 // halves: elements [i, i + P) and [i + pairs, i + pairs + P), two vectors; past
 // the rotated pairs both copy elements [2i, 2i + 2P).
+struct RopeLaunch {
+  int tokens;     // per CTA
+  int cols_inv;   // 65536 / d + 1 of the pairs of a head,
+  int units_inv;  // and of the threads of a head
+};
+
 template <typename T, bool kInterleaved, int P>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_kernel(const __grid_constant__ RopeArgs a, int tokens_per_cta) {
+    rope_kernel(const __grid_constant__ RopeArgs a, const RopeLaunch d) {
   constexpr int kN = kInterleaved ? 2 * P : P;  // elements per vector
-  constexpr int kHeads = 4;                     // heads in flight per thread
+  constexpr int kFlight = kInterleaved ? 6 : 3;  // heads in flight per thread
   using V = Vec<T, kN>;
-  __shared__ float2 cs[kRopeThreads];
+  __shared__ __align__(16) float2 cs[kRopeThreads];
+  const RopeTensor& r = a.t[blockIdx.y];
   const int cols = a.dim / 2;  // table entries per token
-  const int64_t t0 = (int64_t)blockIdx.x * tokens_per_cta;
-  const int n_tok = (int)(a.tokens - t0 < tokens_per_cta ? a.tokens - t0 : tokens_per_cta);
-  for (int i = threadIdx.x; i < n_tok * cols; i += kRopeThreads) {
-    const int tok = i / cols, pair = i - tok * cols;
-    float2 r = make_float2(1.0f, 0.0f);
-    if (pair < a.pairs) {
-      const double turns = (double)a.pos[(t0 + tok) * a.pos_stride + a.axis[pair]] * a.turns[pair];
-      sincospif(2.0f * (float)(turns - rint(turns)), &r.y, &r.x);
-    }
-    cs[i] = r;
-  }
-  __syncthreads();
-  const int units = cols / P, lanes = kRopeThreads / units;
-  const int u = threadIdx.x % units, lane = threadIdx.x / units;
-  if (lane >= lanes) return;
+  const int64_t t0 = (int64_t)blockIdx.x * d.tokens;
+  const int n_tok = (int)(a.tokens - t0 < d.tokens ? a.tokens - t0 : d.tokens);
+  // thread: unit u of the heads lane, lane + step, ... of the CTA's tokens,
+  // counted token by token
+  const int units = cols / P, step = div256(kRopeThreads - 1, d.units_inv) + (kRopeThreads % units == 0);
+  const int lane = div256(threadIdx.x, d.units_inv), u = threadIdx.x - lane * units;
   const int i0 = u * P;
   const bool turned = kInterleaved || i0 < a.pairs;
   const int off0 = kInterleaved ? 2 * i0 : (turned ? i0 : 2 * i0);
   const int off1 = kInterleaved ? 0 : (turned ? i0 + a.pairs : 2 * i0 + P);
-  for (int tok = 0; tok < n_tok; ++tok) {
-    const int64_t t = t0 + tok;
-    for (int h0 = blockIdx.y * lanes * kHeads; h0 < a.heads; h0 += gridDim.y * lanes * kHeads) {
-      V x0[kHeads], x1[kHeads];
-      T* dst[kHeads];
+  const int heads = r.heads, next_tok = r.step_tokens, next_head = r.step_heads;
+  int tok = heads < kRopeThreads ? div256(lane, r.heads_inv) : 0;
+  int head = lane - tok * heads;
+  if (lane >= step) tok = n_tok;  // threads left over
+  const T* src = static_cast<const T*>(r.x) + t0 * r.x_token + off0;
+  T* out = static_cast<T*>(r.out) + t0 * r.out_token + off0;
+  const int second = off1 - off0;
+  V x0[kFlight], x1[kFlight];
+  int at_tok = tok, at_head = head;  // the first of those in flight
+  auto advance = [&](int& t, int& h) {
+    t += next_tok;
+    h += next_head;
+    if (h >= heads) h -= heads, ++t;
+  };
+  auto load = [&]() {
 #pragma unroll
-      for (int k = 0; k < kHeads; ++k) {
-        const int h = h0 + k * lanes + lane;
-        dst[k] = nullptr;
-        if (h >= a.heads) continue;
-        int j = 0;
-        while (h >= a.t[j].head_end) ++j;
-        const RopeTensor& r = a.t[j];
-        const int64_t hh = h - (j ? a.t[j - 1].head_end : 0);
-        const T* src = static_cast<const T*>(r.x) + t * r.x_token + hh * r.x_head;
-        dst[k] = static_cast<T*>(r.out) + t * r.out_token + hh * r.out_head;
-        x0[k] = *reinterpret_cast<const V*>(src + off0);
-        if constexpr (!kInterleaved) x1[k] = *reinterpret_cast<const V*>(src + off1);
+    for (int k = 0; k < kFlight; ++k) {
+      if (tok < n_tok) {
+        const T* p = src + (tok * r.x_token + head * r.x_head);
+        x0[k] = *reinterpret_cast<const V*>(p);
+        if constexpr (!kInterleaved) x1[k] = *reinterpret_cast<const V*>(p + second);
       }
-      const float2* c = cs + tok * cols + i0;
+      advance(tok, head);
+    }
+  };
+  load();
+  if (threadIdx.x < n_tok * cols) {
+    const int t = div256(threadIdx.x, d.cols_inv), pair = threadIdx.x - t * cols;
+    float2 v = make_float2(1.0f, 0.0f);
+    if (pair < a.pairs) {
+      // one entry per lane: as generic loads (the constant cache would serve
+      // the lanes one after the other)
+      double rate;
+      uint32_t axis;
+      asm volatile("ld.f64 %0, [%1];" : "=d"(rate) : "l"(a.turns + pair));
+      asm volatile("ld.u8 %0, [%1];" : "=r"(axis) : "l"(a.axis + pair));
+      const double turns = (double)a.pos[(t0 + t) * a.pos_stride + axis] * rate;
+      sincospif(2.0f * (float)(turns - rint(turns)), &v.y, &v.x);
+    }
+    cs[threadIdx.x] = v;
+  }
+  __syncthreads();
+  // pairs that are not turned are stored as they were read: x * 1 - y * 0 is
+  // not x when y is infinite
+  const int n_turn = min(P, max(0, a.pairs - i0));
+  while (at_tok < n_tok) {
 #pragma unroll
-      for (int k = 0; k < kHeads; ++k) {
-        if (!dst[k]) continue;
-        // pairs that are not turned are stored as they were read: x * 1 - y * 0
-        // is not x when y is infinite
+    for (int k = 0; k < kFlight; ++k) {
+      if (at_tok < n_tok) {
+        float2 c[P];
+        const float2* table = cs + at_tok * cols + i0;
+#pragma unroll
+        for (int p = 0; p < P; ++p) c[p] = table[p];
         if constexpr (kInterleaved) {
 #pragma unroll
           for (int p = 0; p < P; ++p) {
-            const float f0 = to_f32(x0[k].v[2 * p]), f1 = to_f32(x0[k].v[2 * p + 1]);
-            if (i0 + p < a.pairs) {
-              x0[k].v[2 * p] = from_f32<T>(f0 * c[p].x - f1 * c[p].y);
-              x0[k].v[2 * p + 1] = from_f32<T>(f0 * c[p].y + f1 * c[p].x);
-            }
+            const float2 f = pair_of(x0[k].v + 2 * p);
+            if (p < n_turn)
+              set_pair(x0[k].v + 2 * p, f.x * c[p].x - f.y * c[p].y, f.x * c[p].y + f.y * c[p].x);
           }
         } else if (turned) {
+          if constexpr (P > 1) {
 #pragma unroll
-          for (int p = 0; p < P; ++p) {
-            const float f0 = to_f32(x0[k].v[p]), f1 = to_f32(x1[k].v[p]);
-            x0[k].v[p] = from_f32<T>(f0 * c[p].x - f1 * c[p].y);
-            x1[k].v[p] = from_f32<T>(f0 * c[p].y + f1 * c[p].x);
+            for (int p = 0; p < P; p += 2) {
+              const float2 f = pair_of(x0[k].v + p), g = pair_of(x1[k].v + p);
+              set_pair(x0[k].v + p, f.x * c[p].x - g.x * c[p].y, f.y * c[p + 1].x - g.y * c[p + 1].y);
+              set_pair(x1[k].v + p, f.x * c[p].y + g.x * c[p].x, f.y * c[p + 1].y + g.y * c[p + 1].x);
+            }
+          } else {
+            const float f = one_of(x0[k].v), g = one_of(x1[k].v);
+            set_one(x0[k].v, f * c[0].x - g * c[0].y);
+            set_one(x1[k].v, f * c[0].y + g * c[0].x);
           }
         }
-        *reinterpret_cast<V*>(dst[k] + off0) = x0[k];
-        if constexpr (!kInterleaved) *reinterpret_cast<V*>(dst[k] + off1) = x1[k];
+        T* p = out + (at_tok * r.out_token + at_head * r.out_head);
+        *reinterpret_cast<V*>(p) = x0[k];
+        if constexpr (!kInterleaved) *reinterpret_cast<V*>(p + second) = x1[k];
       }
+      advance(at_tok, at_head);
     }
+    load();
   }
 }
 
 template <typename T, bool kInterleaved, int P>
-cudaError_t launch(const RopeArgs& a, cudaStream_t s) {
+cudaError_t launch(RopeArgs& a, cudaStream_t s) {
   // as many tokens per CTA as give each thread one sine and cosine
-  int tokens = kRopeThreads / (a.dim / 2);
-  const int lanes = kRopeThreads / (a.dim / 2 / P);
-  // few tokens: one each, and the heads over several CTAs
-  unsigned gy = 1;
-  if (a.tokens < 148 * tokens) {
-    tokens = 1;
-    gy = (unsigned)((a.heads + lanes * 4 - 1) / (lanes * 4));
-    if (gy > 64) gy = 64;
+  const int cols = a.dim / 2, units = cols / P, step = kRopeThreads / units;
+  const RopeLaunch d{kRopeThreads / cols, 65536 / cols + 1, 65536 / units + 1};
+  for (int i = 0; i < a.n; ++i) {
+    RopeTensor& t = a.t[i];
+    t.step_tokens = step / t.heads;
+    t.step_heads = step % t.heads;
+    t.heads_inv = 65536 / t.heads + 1;
   }
-  const int64_t gx = (a.tokens + tokens - 1) / tokens;
-  rope_kernel<T, kInterleaved, P><<<dim3((unsigned)gx, gy), kRopeThreads, 0, s>>>(a, tokens);
+  const int64_t gx = (a.tokens + d.tokens - 1) / d.tokens;
+  rope_kernel<T, kInterleaved, P><<<dim3((unsigned)gx, (unsigned)a.n), kRopeThreads, 0, s>>>(a, d);
   return cudaGetLastError();
 }
 
@@ -157,14 +196,14 @@ bool fits(const RopeArgs& a, size_t elem, bool interleaved, int P) {
 }
 
 template <typename T, bool kInterleaved>
-cudaError_t pick(const RopeArgs& a, cudaStream_t s) {
+cudaError_t pick(RopeArgs& a, cudaStream_t s) {
   constexpr int kWide = kInterleaved ? 8 / (int)sizeof(T) : 16 / (int)sizeof(T);  // 16 bytes
   if (fits(a, sizeof(T), kInterleaved, kWide)) return launch<T, kInterleaved, kWide>(a, s);
   if constexpr (kWide > 4) {
     if (fits(a, sizeof(T), kInterleaved, 4)) return launch<T, kInterleaved, 4>(a, s);
   }
   if (kInterleaved && !fits(a, sizeof(T), true, 1)) {
-    // element-aligned pairs: the two halves of a pair through separate loads
+    // (the caller has checked the alignment of pairs)
     return cudaErrorMisalignedAddress;
   }
   return launch<T, kInterleaved, 1>(a, s);
@@ -172,7 +211,7 @@ cudaError_t pick(const RopeArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_rope(const RopeArgs& a, bool bf16, bool interleaved, cudaStream_t s) {
+cudaError_t launch_rope(RopeArgs& a, bool bf16, bool interleaved, cudaStream_t s) {
   if (bf16)
     return interleaved ? pick<__nv_bfloat16, true>(a, s) : pick<__nv_bfloat16, false>(a, s);
   return interleaved ? pick<float, true>(a, s) : pick<float, false>(a, s);
