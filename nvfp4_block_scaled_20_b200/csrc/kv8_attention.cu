@@ -25,6 +25,7 @@
 // Long caches are cut into runs of equal length over CTAs; runs past a
 // sequence's end return at once, so ragged batches spread evenly.
 #include "attention_common.cuh"
+#include "kernels.h"
 
 namespace nvfp4 {
 
@@ -33,6 +34,7 @@ namespace {
 constexpr int kStepKeys = 64;
 constexpr int kDepth = 4;     // steps in flight
 constexpr int kWarps = 4;     // consumer warps
+constexpr int kLeastRun = 2, kWaveRun = 32;  // steps of a CTA
 constexpr int kRowThreads = (kWarps + 1) * 32;
 
 struct RowsPlan {
@@ -461,10 +463,14 @@ RowsPlan plan_rows(int32_t heads, int32_t group, int32_t n, int32_t max_rows, in
   p.rows = (int64_t)max_rows * group <= 8 ? 8 : 16;
   p.row_tiles = (int)(((int64_t)max_rows * group + p.rows - 1) / p.rows);
   const int64_t steps = (max_len + kStepKeys - 1) / kStepKeys;
-  // about three waves of CTAs at full length, runs of 2 to 64 steps
+  // One wave of CTAs (three per SM) while that keeps the runs short: a CTA's
+  // start costs as much as several steps.  Longer caches get about three waves
+  // at full length, since the sequences of a batch are seldom all that long.
+  const int64_t slots = 3 * (int64_t)num_sms();
   const int64_t all = (int64_t)n * heads * p.row_tiles * steps;
-  int64_t run = all / (148 * 4 * 3);
-  run = run < 2 ? 2 : (run > 64 ? 64 : run);
+  int64_t run = (all + slots - 1) / slots;
+  if (run > kWaveRun) run = run / 3 > kWaveRun ? run / 3 : kWaveRun;
+  run = run < kLeastRun ? kLeastRun : (run > 64 ? 64 : run);
   p.run = (int)run;
   p.splits = (int)((steps + run - 1) / run);
   if (p.splits < 1) p.splits = 1;

@@ -62,7 +62,7 @@ template <typename T, bool kInterleaved, int P>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeArgs a, const RopeLaunch d) {
   constexpr int kN = kInterleaved ? 2 * P : P;  // elements per vector
-  constexpr int kFlight = kInterleaved ? 6 : 3;  // heads in flight per thread
+  constexpr int kFlight = 2;  // heads in flight per thread
   using V = Vec<T, kN>;
   __shared__ __align__(16) float2 cs[kRopeThreads];
   const RopeTensor& r = a.t[blockIdx.y];
