@@ -32,6 +32,8 @@ constexpr uint32_t kDevErrShape = 2u;  // NVFP4_ERR_SHAPE
 // (in log2): rescaling the accumulators is rare, and weights stay <= 2^8, far
 // inside fp16.
 constexpr float kLazy = 8.0f;
+// Where a maximum is found too late for that, weights may grow to 2^15.
+constexpr float kJump = 15.0f;
 constexpr float kNegInf = -INFINITY;
 
 // ------------------------------------------------------------ PTX wrappers

@@ -32,17 +32,12 @@ namespace {
 constexpr int kKeys = 128;   // keys per step
 constexpr int kHalf = 128;   // rows per half (tensor-memory lanes)
 constexpr int kTileRows = 2 * kHalf;
-constexpr int kSlots = 5;    // ring of K and V tiles
+constexpr int kSlots = 4;    // ring of K and V tiles in fp16
+constexpr int kRaw = 2;      // ring of tiles as they lie in the pages
 constexpr int kInfo = 4;     // ring of a step's scales
-constexpr int kTileThreads = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 12;
+constexpr int kTileThreads = 12 * 32;
+constexpr int kLoadWarp = 8, kLoadWarps = 2, kMmaWarp = 10, kCopyWarp = 11;
 constexpr uint32_t kTmemCols = 512;
-// One pair of weights in kPolyEvery takes its powers of two from the FMA pipe:
-// the special-function unit's 4 results per clock and SM quarter would take as
-// long for all of them as the tensor pipe takes for the products.
-constexpr int kPolyEvery = 4;
-constexpr float kPoly0 = 0x1.000002p+0f, kPoly1 = 0x1.62e430p-1f, kPoly2 = 0x1.ebf906p-3f,
-                kPoly3 = 0x1.c6af6cp-5f, kPoly4 = 0x1.3d1070p-7f, kPoly5 = 0x1.5f0890p-10f;
 // Tensor-memory columns of a half's scores (and weights) and sums.
 __host__ __device__ constexpr uint32_t col_s(int h) { return 128u * h; }
 __host__ __device__ constexpr uint32_t col_o(int h) { return 256u + 128u * h; }
@@ -55,8 +50,9 @@ struct TilesPlan {
 
 struct TilesSmem {  // after the q tiles and the ring
   float4 info[kInfo][4];  // per 32 keys of a step: ks, log2 vs, 1 / vs
-  uint64_t kv_full[kSlots], kv_empty[kSlots];
-  uint64_t q_full, s_full[2], p_half[2], p_full[2], o_full[2], mma_done;
+  uint64_t kv_full[kSlots], kv_empty[kSlots], raw_full[kRaw], raw_empty[kRaw];
+  int whole[kInfo];  // every key of the step is in the cache and seen by a row
+  uint64_t q_full, s_full[2], p_part[2], p_full[2], pv_part[2], o_full[2], mma_done;
   uint32_t tmem;
   int gave_up;
 };
@@ -64,7 +60,7 @@ template <int kDim>
 __host__ __device__ constexpr int tile_bytes() { return kKeys * kDim * 2; }
 template <int kDim>
 constexpr int tiles_smem_bytes() {
-  return (2 + kSlots) * tile_bytes<kDim>() + (int)sizeof(TilesSmem) + 1024;
+  return (2 + kSlots) * tile_bytes<kDim>() + kRaw * tile_bytes<kDim>() / 2 + (int)sizeof(TilesSmem) + 1024;
 }
 
 // --------------------------------------------------------------- tcgen05
@@ -135,12 +131,16 @@ __device__ __forceinline__ void ld32(uint32_t addr, uint32_t* r) {
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void st32(uint32_t addr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-      NVFP4_I8(r, 0), NVFP4_I8(r, 8), NVFP4_I8(r, 16), NVFP4_I8(r, 24)
-      : "memory");
+__device__ __forceinline__ void ld8(uint32_t addr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : NVFP4_R8(r, 0)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void st8(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+               NVFP4_I8(r, 0)
+               : "memory");
 }
 __device__ __forceinline__ void st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -200,38 +200,16 @@ __device__ __forceinline__ void store_bf16x8(__nv_bfloat16* dst, const uint32_t*
   *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t below(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+}
+
 // max(a, b, c), NaN when one of them is.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-
-// Two powers of two on the FMA pipe.  x = n + f, n whole, |f| <= 1/2 (adding
-// 1.5 2^23 rounds to n and leaves it in the low bits); 2^f by the polynomial of
-// degree 5 that interpolates it at the Chebyshev nodes of [-1/2, 1/2] (relative
-// error below 2.5e-7); n goes into the exponent.  x is at most 2^6 here; below
-// -125 it gives 2^-125, which no fp16 weight and no sum notices.
-__device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
-  float a, b;
-  unpack2(x, a, b);
-  x = pack2(fmaxf(a, -125.0f), fmaxf(b, -125.0f));
-  const uint64_t r = add2(x, pack2(12582912.0f, 12582912.0f));
-  const uint64_t f = sub2(x, sub2(r, pack2(12582912.0f, 12582912.0f)));
-  uint64_t p = pack2(kPoly5, kPoly5);
-  p = fma2(p, f, pack2(kPoly4, kPoly4));
-  p = fma2(p, f, pack2(kPoly3, kPoly3));
-  p = fma2(p, f, pack2(kPoly2, kPoly2));
-  p = fma2(p, f, pack2(kPoly1, kPoly1));
-  p = fma2(p, f, pack2(kPoly0, kPoly0));
-  float r0, r1, p0, p1;
-  unpack2(r, r0, r1);
-  unpack2(p, p0, p1);
-  // n 2^23 + p as integers; a multiply-add, on the FMA pipe too
-  uint32_t b0, b1;
-  asm("mad.lo.u32 %0, %1, 0x800000, %2;" : "=r"(b0) : "r"(__float_as_uint(r0)), "r"(__float_as_uint(p0)));
-  asm("mad.lo.u32 %0, %1, 0x800000, %2;" : "=r"(b1) : "r"(__float_as_uint(r1)), "r"(__float_as_uint(p1)));
-  return pack2(__uint_as_float(b0), __uint_as_float(b1));
 }
 
 // A work unit: a tile, its steps, and its part (-1: the whole tile).
@@ -268,7 +246,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   uint8_t* sq = smem;              // two q tiles
   uint8_t* ring = smem + 2 * kTile;
-  TilesSmem& sm = *reinterpret_cast<TilesSmem*>(ring + kSlots * kTile);
+  uint8_t* raw = ring + kSlots * kTile;  // kRaw tiles of codes
+  TilesSmem& sm = *reinterpret_cast<TilesSmem*>(raw + kRaw * kTile / 2);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pt = a.c.page_tokens;
 
@@ -293,14 +272,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int n_steps = s1 - s0;
 
   if (threadIdx.x == 0) {
+    for (int i = 0; i < kRaw; ++i) {
+      bar_init(smem_addr(&sm.raw_full[i]), 1);
+      bar_init(smem_addr(&sm.raw_empty[i]), kLoadWarps);
+    }
     for (int i = 0; i < kSlots; ++i) {
-      bar_init(smem_addr(&sm.kv_full[i]), 4);
+      bar_init(smem_addr(&sm.kv_full[i]), kLoadWarps);
       bar_init(smem_addr(&sm.kv_empty[i]), 1);
     }
     bar_init(smem_addr(&sm.q_full), 4 * halves);
     for (int h = 0; h < 2; ++h) {
       bar_init(smem_addr(&sm.s_full[h]), 1);
-      bar_init(smem_addr(&sm.p_half[h]), 4);
+      bar_init(smem_addr(&sm.p_part[h]), 4);
+      bar_init(smem_addr(&sm.pv_part[h]), 1);
       bar_init(smem_addr(&sm.p_full[h]), 4);
       bar_init(smem_addr(&sm.o_full[h]), 1);
     }
@@ -369,7 +353,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       // keys that every row of the warp sees
       const int all_lo = seen_at(a, q.len, __reduce_max_sync(0xFFFFFFFFu, at)).lo;
       const int all_hi = seen_at(a, q.len, __reduce_min_sync(0xFFFFFFFFu, at)).hi;
-      float m = kNegInf, l = 0.0f;
+      float m = kNegInf, l = 0.0f, pending = kNegInf;
       bool ok = true;
       for (int j = 0; j < n_steps; ++j) {
         const int key0 = step_at(steps, s0 + j) * kKeys;
@@ -380,20 +364,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         fence_after();
         const bool masked = key0 < all_lo || key0 + kKeys > all_hi;
         const float4* info = sm.info[j % kInfo];
-        // Two passes over the scores in tensor memory, 32 columns at a time in
-        // two buffers, the next 32 on the way while these are worked on.  (All
-        // 128 in registers, unrolled, overran the instruction cache.)
-        uint32_t s0_[32], s1_[32];
+        // Scores of 32 columns, three at a time.  (Registers are what limits it:
+        // spills are slow beside so much shared memory, which leaves little of
+        // the L1 cache.)
+        uint32_t s0_[32], s1_[32], s2_[32];
         auto hide = [&](uint32_t* s, int key) {
           const Seen see = seen_at(a, q.len, at);
+          const uint32_t bits = (below(see.hi - key) & ~below(see.lo - key)) | below(see.sink - key);
 #pragma unroll
           for (int k = 0; k < 32; ++k)
-            if (!((key + k >= see.lo && key + k < see.hi) || key + k < see.sink))
-              s[k] = __float_as_uint(kNegInf);
+            if (!(bits >> k & 1)) s[k] = __float_as_uint(kNegInf);
         };
-        float top = kNegInf;
-        auto maximum = [&](uint32_t* s, int c) {
-          if (masked) hide(s, key0 + 32 * c);
+        auto maximum = [&](const uint32_t* s, int c) {
           const float4 x = info[c];
           float t[4];
 #pragma unroll
@@ -410,43 +392,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           t[1] = max3(t[1], __uint_as_float(s[23]), __uint_as_float(s[31]));
           t[0] = max3(t[0], t[1], max3(t[2], t[2], t[3]));
           // the factor is never 0: masked scores (-inf) stay -inf
-          top = max3(top, top, fmaf(t[0], fmaxf(crow * x.x, 1e-37f), x.y));
+          return fmaf(t[0], fmaxf(crow * x.x, 1e-37f), x.y);
         };
-        ld32(ts, s0_);
-        ld_wait<32>(s0_);
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          ld32(ts + 32 * (c + 1), s1_);
-          maximum(s0_, c);
-          ld_wait<32>(s1_);
-          ld32(ts + 32 * ((c + 2) & 3), s0_);  // at last the first for the second pass
-          maximum(s1_, c + 1);
-          ld_wait<32>(s0_);
-        }
-        // a NaN among the scores that a row sees makes its maximum, and with it
-        // the whole row, NaN
-        if (__any_sync(0xFFFFFFFFu, !(top <= m + kLazy))) {
-          const float next = max3(m, m, top);
-          const float g = m == kNegInf ? 0.0f : exp2_approx(m - next);
-          m = next;
-          l *= g;
-          if (j > 0) {
-            // the products of the steps before are complete: this step's
-            // scores were issued after them
-#pragma unroll 1
-            for (int c = 0; c < kDim; c += 32) {
-              ld32(to + c, s1_);
-              ld_wait<32>(s1_);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) s1_[k] = __float_as_uint(__uint_as_float(s1_[k]) * g);
-              st32(to + c, s1_);
-            }
-          }
-        }
-        const float base = m == kNegInf ? 0.0f : m;
+        float base = 0.0f;
         // the weights of 32 columns, written over scores already read
-        auto weights = [&](uint32_t* s, int c) {
-          if (masked) hide(s, key0 + 32 * c);
+        auto weights = [&](const uint32_t* s, int c) {
           const float4 x = info[c];
           const float f = fmaxf(crow * x.x, 1e-37f);
           const uint64_t ff = pack2(f, f), bb = pack2(x.y - base, x.y - base);
@@ -454,18 +404,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           uint64_t sum = pack2(0.0f, 0.0f);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            uint64_t t = fma2(pack2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ff, bb);
             float x0, x1;
-            if (k % kPolyEvery == kPolyEvery - 1) {
-              t = exp2_poly(t);
-              unpack2(t, x0, x1);
-            } else {
-              unpack2(t, x0, x1);
-              x0 = exp2_approx(x0);
-              x1 = exp2_approx(x1);
-              t = pack2(x0, x1);
-            }
-            sum = add2(sum, t);
+            unpack2(fma2(pack2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), ff, bb), x0, x1);
+            x0 = exp2_approx(x0);
+            x1 = exp2_approx(x1);
+            sum = add2(sum, pack2(x0, x1));
             p[k] = f16x2(x0, x1);
           }
           st16(ts + 16 * c, p);
@@ -473,23 +416,70 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           unpack2(sum, a0, a1);
           l = fmaf(a0 + a1, x.z, l);
         };
+        // Moves the row's maximum to at least `top` where it has to.  A NaN among
+        // the scores that a row sees makes its maximum, and with it the whole
+        // row, NaN.
+        auto raise = [&](float top, float slack, bool late) {
+          if (!__any_sync(0xFFFFFFFFu, !(top <= m + slack))) return;
+          if (late) ok = warp_wait(smem_addr(&sm.pv_part[h]), j & 1, gave_up, a.wait_limit_ns);
+          fence_after();
+          const float next = max3(m, m, top);
+          const float g = m == kNegInf ? 0.0f : exp2_approx(m - next);
+          m = next;
+          l *= g;
+          if (j == 0 && !late) return;
+          // the products issued so far are complete: this step's scores came
+          // after those of the steps before
 #pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {
-          ld32(ts + 32 * (c + 1), s1_);
-          weights(s0_, c);
-          ld_wait<32>(s1_);
-          if (c == 0) ld32(ts + 64, s0_);
-          weights(s1_, c + 1);
-          if (c == 0) ld_wait<32>(s0_);
-          // the product with V starts on the first half's weights
+          for (int c = 0; c < kDim; c += 8) {
+            uint32_t o[8];
+            ld8(to + c, o);
+            asm volatile("tcgen05.wait::ld.sync.aligned;"
+                         : "+r"(o[0]), "+r"(o[1]), "+r"(o[2]), "+r"(o[3]), "+r"(o[4]), "+r"(o[5]),
+                           "+r"(o[6]), "+r"(o[7])::"memory");
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * g);
+            st8(to + c, o);
+          }
+        };
+        auto hand_over = [&](uint64_t* bar) {
           st_wait();
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive(smem_addr(c == 0 ? &sm.p_half[h] : &sm.p_full[h]));
+          if (lane == 0) bar_arrive(smem_addr(bar));
+        };
+        ld32(ts, s0_);
+        ld32(ts + 32, s1_);
+        ld32(ts + 64, s2_);
+        ld_wait<32>(s0_);
+        ld_wait<32>(s1_);
+        ld_wait<32>(s2_);
+        if (masked) {
+          hide(s0_, key0);
+          hide(s1_, key0 + 32);
+          hide(s2_, key0 + 64);
         }
+        // The first 96 keys' weights go to the tensor pipe while the last 32 are
+        // worked on.  Their maximum only moves the row's own with the next
+        // step's, unless fp16 weights could overflow: the product of the first
+        // 96 is under way by then.
+        raise(max3(pending, maximum(s0_, 0), max3(maximum(s1_, 1), maximum(s2_, 2), kNegInf)), kLazy,
+              false);
+        base = m == kNegInf ? 0.0f : m;
+        weights(s0_, 0);
+        ld32(ts + 96, s0_);
+        weights(s1_, 1);
+        weights(s2_, 2);
+        hand_over(&sm.p_part[h]);
+        ld_wait<32>(s0_);
+        if (masked) hide(s0_, key0 + 96);
+        pending = maximum(s0_, 3);
+        raise(pending, kJump, true);
+        if (!ok) break;
+        base = m == kNegInf ? 0.0f : m;
+        weights(s0_, 3);
+        hand_over(&sm.p_full[h]);
       }
-      // nothing seen: what the polynomial gave for masked keys is no weight
-      if (m == kNegInf) l = 0.0f;
       if (ok && n_steps > 0 &&
           !warp_wait(smem_addr(&sm.o_full[h]), 0, gave_up, a.wait_limit_ns))
         ok = false;
@@ -548,9 +538,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             l == 0.0f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
     }
   } else if (warp < kMmaWarp) {
-    // ---------------------------------------------------------------- loaders
+    // ------------------------------------------------------------- converters
     constexpr int kLanesRow = kDim / 16;             // lanes per key
-    constexpr int kRowsLoad = 4 * 32 / kLanesRow;    // keys per load of the four warps
+    constexpr int kRowsLoad = kLoadWarps * 32 / kLanesRow;  // keys per load of the warps
     constexpr int kLoads = kKeys / kRowsLoad;
     const int w = warp - kLoadWarp;
     // The eight lanes of a shared-memory store phase write eight different
@@ -558,89 +548,40 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // rows.  The lanes' columns 4..7 go to the upper half of the warp.
     const int row = w * (32 / kLanesRow) + (kDim == 128 ? (lane >> 2) & 3 : lane >> 2);
     const int col = (lane & 3) + (kDim == 128 ? (lane >> 4) * 4 : 0);
-    const int pt_log = 31 - __clz(pt);            // 5, 6 or 7
-    const int step_log = 7 - pt_log;              // pages per step, as a power of two
-    const int group = 32 >> step_log;             // steps per look-up of pages
     const Seen first = seen_by(a, q, i_first), last = seen_by(a, q, i_last);
-    int looked = 0;   // steps [looked, looked + group) are looked up:
-    int block = -1;   // each lane's page of them, as its block of codes
-    bool all_here = false;  // no page of the looked-up steps lies outside the cache
-    float ks = 0.0f, vs = -1.0f;  // lanes 0..3: of the step's 32-key groups
-    auto look_up = [&](int step) {
-      looked = step;
-      block = -1;
-      bool bad = false;
-      const int mine = step + (lane >> step_log);
-      if (mine < s1) {
-        const int key =
-            step_at(steps, mine) * kKeys + ((lane & ((1 << step_log) - 1)) << pt_log);
-        if (key < q.len) {
-          const int page = a.b.table[unit.seq * a.b.table_stride + (key >> pt_log)];
-          if (page < 0 || page >= a.c.pages) {
-            atomicOr(a.err, kDevErrShape);
-            bad = true;
-          } else {
-            block = page;
-          }
-        }
-      }
-      all_here = !__any_sync(0xFFFFFFFFu, bad);
-    };
-    // one tile's codes: 16 bytes of kLoads keys
-    auto load = [&](uint4* raw, int step, int which) {
-      const int key0 = step_at(steps, step) * kKeys;
-      const bool whole = (key0 >= first.lo && key0 + kKeys <= last.hi) || key0 + kKeys <= last.sink;
-      const uint8_t* from = nullptr;
-      bool here = false;
-      // the next page, every 32, 64 or 128 keys
-      auto turn = [&](int k) {
-        const int pg = __shfl_sync(0xFFFFFFFFu, block,
-                                   ((step - looked) << step_log) + (k * kRowsLoad >> pt_log));
-        here = pg >= 0;
-        from = a.c.codes[which] + ((int64_t)pg * a.c.heads + unit.head) * (pt * kDim) + row * kDim +
-               col * 16;
-      };
-      if (whole && all_here) {
+    bool ok = true;
+    for (int n = 0; n < 2 * n_steps; ++n) {
+      const int slot = n % kSlots, from = n % kRaw, j = n >> 1;
+      ok = warp_wait(smem_addr(&sm.kv_empty[slot]), ((n / kSlots) & 1) ^ 1, gave_up, a.wait_limit_ns) &&
+           warp_wait(smem_addr(&sm.raw_full[from]), (n / kRaw) & 1, gave_up, a.wait_limit_ns);
+      if (!ok) break;
+      const uint8_t* codes = raw + from * (kTile / 2) + row * kDim + col * 16;
+      uint4 x[kLoads];
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        x[k] = *reinterpret_cast<const uint4*>(codes + k * kRowsLoad * kDim);
+      if (!sm.whole[j % kInfo]) {
+        // codes that no row of the tile sees, or that were not copied, may be
+        // anything, NaN among it
+        const int key0 = step_at(steps, s0 + j) * kKeys;
 #pragma unroll
         for (int k = 0; k < kLoads; ++k) {
-          const int in_page = (k * kRowsLoad) & (pt - 1);
-          if (in_page == 0) turn(k);
-          raw[k] = __ldg(reinterpret_cast<const uint4*>(from + in_page * kDim));
+          const int in = k * kRowsLoad + row, key = key0 + in;
+          const bool want = sm.info[j % kInfo][in >> 5].y != kNegInf &&
+                            ((key >= first.lo && key < last.hi) || key < last.sink);
+          if (!want) x[k] = make_uint4(0, 0, 0, 0);
         }
-        return;
       }
-#pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        const int in_page = (k * kRowsLoad) & (pt - 1);
-        if (in_page == 0) turn(k);
-        const int key = key0 + k * kRowsLoad + row;
-        // codes that no row of the tile sees may be anything, NaN among it
-        const bool want =
-            here && (whole || (key >= first.lo && key < last.hi) || key < last.sink);
-        raw[k] = load_if(from + in_page * kDim, want);
-      }
-    };
-    auto scales = [&](int step) {
-      const int pg =
-          __shfl_sync(0xFFFFFFFFu, block, ((step - looked) << step_log) + ((lane & 3) * 32 >> pt_log));
-      ks = 0.0f;
-      vs = -1.0f;
-      if (w == 0 && lane < 4 && pg >= 0) {
-        ks = a.c.scales[0][(int64_t)pg * a.c.heads + unit.head];
-        vs = a.c.scales[1][(int64_t)pg * a.c.heads + unit.head];
-      }
-    };
-    auto store = [&](const uint4* raw, int slot) {
       uint8_t* to = ring + slot * kTile + (col >> 2) * kBlock;
       const int chunk = (2 * col) & 7;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
-        const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+        const uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
         uint32_t f[8];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          f[2 * t] = e4m3x2_f16x2(x[t] & 0xFFFFu);
-          f[2 * t + 1] = e4m3x2_f16x2(x[t] >> 16);
+          f[2 * t] = e4m3x2_f16x2(y[t] & 0xFFFFu);
+          f[2 * t + 1] = e4m3x2_f16x2(y[t] >> 16);
         }
         const int at = k * kRowsLoad + row;
         *reinterpret_cast<uint4*>(to + chunk_at(at, chunk)) = make_uint4(f[0], f[1], f[2], f[3]);
@@ -648,49 +589,105 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&sm.kv_full[slot]));
-    };
-    auto wait_slot = [&](int n) {
-      return warp_wait(smem_addr(&sm.kv_empty[n % kSlots]), ((n / kSlots) & 1) ^ 1, gave_up,
-                       a.wait_limit_ns);
-    };
-    // K and V each have a tile's loads in flight: a step's time to arrive
-    uint4 rk[kLoads], rv[kLoads];
-    bool ok = true;
-    if (n_steps > 0) {
-      look_up(s0);
-      scales(s0);
-      load(rk, s0, 0);
-      load(rv, s0, 1);
-    }
-    for (int j = 0; j < n_steps; ++j) {
-      const int next = s0 + j + 1;
-      if (!wait_slot(2 * j)) {
-        ok = false;
-        break;
+      if (lane == 0) {
+        bar_arrive(smem_addr(&sm.raw_empty[from]));
+        bar_arrive(smem_addr(&sm.kv_full[slot]));
       }
-      if (w == 0 && lane < 4) {
-        // an absent page: its keys' scores become -inf
-        const float lv = vs < 0.0f ? kNegInf : (float)((int)(__float_as_uint(vs) >> 23) - 127);
-        sm.info[j % kInfo][lane] = make_float4(ks, lv, vs < 0.0f ? 0.0f : 1.0f / vs, 0.0f);
-      }
-      store(rk, (2 * j) % kSlots);
-      if (next < s1) {
-        if (next >= looked + group) look_up(next);
-        scales(next);
-        load(rk, next, 0);
-      }
-      if (!wait_slot(2 * j + 1)) {
-        ok = false;
-        break;
-      }
-      store(rv, (2 * j + 1) % kSlots);
-      if (next < s1) load(rv, next, 1);
     }
     if (!ok) {
       *gave_up = 1;
       if (lane == 0) atomicOr(a.err, kDevErrTimeout);
     }
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------------------------ copies
+    const int pt_log = 31 - __clz(pt);            // 5, 6 or 7
+    const int step_log = 7 - pt_log;              // pages per step, as a power of two
+    const int pieces = 1 << step_log, group = 32 >> step_log;  // steps per look-up
+    const uint32_t piece_bytes = (uint32_t)pt * kDim;
+    const Seen first = seen_by(a, q, i_first), last = seen_by(a, q, i_last);
+    // Each lane holds one of the next 32 pages and its scales; the following
+    // ones are on the way, the scales a step after the pages: a look-up is two
+    // dependent loads from memory, longer than a step.
+    int looked = 0, page = -1, next_page = -1;
+    float ks = 0.0f, vs = -1.0f, next_ks = 0.0f, next_vs = -1.0f;
+    auto fetch_pages = [&](int step) {
+      next_page = -1;
+      const int mine = step + (lane >> step_log);
+      if (mine < s1) {
+        const int key = step_at(steps, mine) * kKeys + ((lane & (pieces - 1)) << pt_log);
+        // pages past the sequence's end are not looked up
+        if (key < q.len) {
+          next_page = a.b.table[unit.seq * a.b.table_stride + (key >> pt_log)];
+          if (next_page < 0 || next_page >= a.c.pages) {
+            atomicOr(a.err, kDevErrShape);
+            next_page = -1;
+          }
+        }
+      }
+    };
+    auto fetch_scales = [&]() {
+      next_ks = 0.0f;
+      next_vs = -1.0f;
+      if (next_page >= 0) {
+        next_ks = a.c.scales[0][(int64_t)next_page * a.c.heads + unit.head];
+        next_vs = a.c.scales[1][(int64_t)next_page * a.c.heads + unit.head];
+      }
+    };
+    fetch_pages(s0);
+    fetch_scales();
+    bool ok = true;
+    int n = 0;
+    for (int j = 0; j < n_steps && ok; ++j) {
+      if (j == 0 || s0 + j == looked + group) {
+        looked = s0 + j;
+        page = next_page;
+        ks = next_ks;
+        vs = next_vs;
+        fetch_pages(looked + group);
+      } else if (s0 + j == looked + 1) {
+        fetch_scales();
+      }
+      const int base = (s0 + j - looked) << step_log;
+      const bool mine = lane >= base && lane < base + pieces;
+      const uint32_t here = __ballot_sync(0xFFFFFFFFu, mine && page >= 0);
+      for (int which = 0; which < 2; ++which, ++n) {
+        const int to = n % kRaw;
+        ok = warp_wait(smem_addr(&sm.raw_empty[to]), ((n / kRaw) & 1) ^ 1, gave_up, a.wait_limit_ns);
+        if (!ok) break;
+        if (which == 0) {
+          // the scales of the step's four groups of 32 keys
+          const int from = base + ((lane & 3) * 32 >> pt_log);
+          const float k1 = __shfl_sync(0xFFFFFFFFu, ks, from), v1 = __shfl_sync(0xFFFFFFFFu, vs, from);
+          if (lane < 4) {
+            // an absent page: its keys' scores become -inf
+            const float lv = v1 < 0.0f ? kNegInf : (float)((int)(__float_as_uint(v1) >> 23) - 127);
+            sm.info[j % kInfo][lane] = make_float4(k1, lv, v1 < 0.0f ? 0.0f : 1.0f / v1, 0.0f);
+          }
+          if (lane == 0) {
+            const int key0 = step_at(steps, s0 + j) * kKeys;
+            sm.whole[j % kInfo] =
+                __popc(here) == pieces &&
+                ((key0 >= first.lo && key0 + kKeys <= last.hi) || key0 + kKeys <= last.sink);
+          }
+        }
+        __syncwarp();
+        const uint32_t full = smem_addr(&sm.raw_full[to]);
+        if (lane == 0) bar_expect(full, __popc(here) * piece_bytes);
+        __syncwarp();
+        if (mine && page >= 0)
+          bulk_copy(smem_addr(raw) + to * (kTile / 2) + (lane - base) * piece_bytes,
+                    a.c.codes[which] + ((int64_t)page * a.c.heads + unit.head) * piece_bytes,
+                    piece_bytes, full);
+        __syncwarp();
+      }
+    }
+    if (!ok) {
+      *gave_up = 1;
+      if (lane == 0) atomicOr(a.err, kDevErrTimeout);
+    }
+    // no copy may land after the CTA is gone
+    for (int i = max(0, n - kRaw); i < n; ++i)
+      bar_wait(smem_addr(&sm.raw_full[i % kRaw]), (i / kRaw) & 1, nullptr, 200000000ull);
   } else {
     // -------------------------------------------------------------------- MMA
     if (warp == kMmaWarp) {
@@ -712,23 +709,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         commit(smem_addr(&sm.s_full[h]), lead);
       };
-      // O of half h += P V over 64 keys of the V tile n
-      auto output = [&](int h, int n, int part, bool first_step) {
+      // O of half h += P V over keys 16 k0 .. 16 k1 of the V tile n
+      auto output = [&](int h, int n, int k0, int k1, bool first_step) {
         const uint32_t vb = operand(ring_at + (n % kSlots) * kTile, kBlock);
 #pragma unroll
-        for (int i = 0; i < kKeys / 32; ++i) {
-          const int k = part * (kKeys / 32) + i;
+        for (int k = k0; k < k1; ++k)
           mma_ts(tmem + col_o(h), tmem + col_s(h) + 8 * k, vb + (uint32_t)(k * (2048 >> 4)), kInstrO,
                  !first_step || k > 0, lead);
-        }
       };
       bool ok = true;
       if (n_steps > 0) {
         ok = warp_wait(smem_addr(&sm.q_full), 0, gave_up, a.wait_limit_ns) && wait_tile(0);
         if (ok) {
           fence_after();
-          for (int h = 0; h < halves; ++h) scores(h, 0);
-          commit(smem_addr(&sm.kv_empty[0]), lead);
+          scores(0, 0);
+          if (halves == 1) commit(smem_addr(&sm.kv_empty[0]), lead);
         }
       }
       for (int j = 0; j < n_steps && ok; ++j) {
@@ -736,18 +731,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const bool more = j + 1 < n_steps;
         for (int h = 0; h < halves && ok; ++h) {
           if ((h == 0 && !wait_tile(nv)) ||
-              !warp_wait(smem_addr(&sm.p_half[h]), j & 1, gave_up, a.wait_limit_ns)) {
+              !warp_wait(smem_addr(&sm.p_part[h]), j & 1, gave_up, a.wait_limit_ns)) {
             ok = false;
             break;
           }
           fence_after();
-          output(h, nv, 0, j == 0);
+          output(h, nv, 0, 6, j == 0);
+          commit(smem_addr(&sm.pv_part[h]), lead);
           if (!warp_wait(smem_addr(&sm.p_full[h]), j & 1, gave_up, a.wait_limit_ns)) {
             ok = false;
             break;
           }
           fence_after();
-          output(h, nv, 1, false);
+          output(h, nv, 6, 8, false);
           if (h == halves - 1) commit(smem_addr(&sm.kv_empty[nv % kSlots]), lead);
           if (more) {
             if (h == 0 && !wait_tile(nk)) {
@@ -759,6 +755,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (h == halves - 1) commit(smem_addr(&sm.kv_empty[nk % kSlots]), lead);
           } else {
             commit(smem_addr(&sm.o_full[h]), lead);
+          }
+          if (j == 0 && h == 0 && halves == 2) {
+            // the second half starts when the first has its first weights: from
+            // then on the halves take turns, one in the softmax and one on the
+            // tensor pipe
+            scores(1, 0);
+            commit(smem_addr(&sm.kv_empty[0]), lead);
           }
         }
       }
