@@ -165,11 +165,19 @@ nvfp4_status nvfp4_kv8_read(const nvfp4_kv8_cache* cache, const nvfp4_kv8_batch*
   return write_or_read(false, cache, batch, dtype, k, v, strides, ws, ws_bytes, stream);
 }
 
+namespace {
+// Tiles of query rows over all sequences and KV heads, each a CTA or several:
+// at most 2^30.
+inline bool tiles_ok(int64_t heads, int64_t group, int64_t n, int64_t max_rows) {
+  return max_rows * group <= (1 << 30) && (max_rows * group + 255) / 256 * heads * n <= (1 << 30);
+}
+}  // namespace
+
 size_t nvfp4_kv8_attention_workspace_bytes(int32_t heads, int32_t head_dim, int32_t page_tokens,
                                            int32_t q_heads, int32_t n, int32_t max_rows,
                                            int32_t table_pages) {
   if (heads < 1 || q_heads < heads || q_heads % heads || n < 1 || max_rows < 1 || table_pages < 1 ||
-      page_tokens < 1)
+      page_tokens < 1 || head_dim < 1 || !tiles_ok(heads, q_heads / heads, n, max_rows))
     return kPartOffset;
   return kPartOffset + kv8_attention_partial_bytes(heads, head_dim, q_heads / heads, n, max_rows,
                                                    (int64_t)table_pages * page_tokens);
@@ -188,7 +196,7 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
     return NVFP4_ERR_INVALID_ARG;
   if (qp->q_heads < cache->heads || qp->q_heads % cache->heads) return NVFP4_ERR_SHAPE;
   const int64_t group = qp->q_heads / cache->heads;
-  if ((int64_t)batch->max_rows * group > (1 << 30)) return NVFP4_ERR_SHAPE;
+  if (!tiles_ok(cache->heads, group, batch->n, batch->max_rows)) return NVFP4_ERR_SHAPE;
   if (batch->n == 0 || batch->rows == 0 || batch->max_rows == 0) return NVFP4_OK;
   if (!qp->q || !qp->out) return NVFP4_ERR_INVALID_ARG;
   const int64_t strides[4] = {qp->q_token_stride, qp->q_head_stride, qp->out_token_stride,

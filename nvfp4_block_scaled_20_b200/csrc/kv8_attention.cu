@@ -504,14 +504,19 @@ cudaError_t launch_rows(const Kv8Attention& a, const RowsPlan& p, cudaStream_t s
 }  // namespace
 
 namespace {
-// Rows of a KV head above which tiles of 256 rows on the tensor pipe are
-// faster than 16-row tiles that each read the cache.
-inline bool many_rows(int64_t max_rows, int32_t group) { return max_rows * group > 64; }
+// Whether tiles of 256 rows on the tensor pipe are faster than tiles of 16 rows
+// that each read the cache.  Measured at 8 sequences of 4100..8200 tokens, 4 KV
+// heads (tiles of 256 / of 16 rows, us): dim 128, 24 rows 42 / 52, 48 rows 43 /
+// 67; dim 64, 24 rows 37 / 25, 48 rows 37 / 32, 66 rows 38 / 61.  So above one
+// tile of 16 rows at 128 and above two at 64.
+inline bool many_rows(int32_t dim, int64_t max_rows, int32_t group) {
+  return max_rows * group * dim > 2048;
+}
 }  // namespace
 
 size_t kv8_attention_partial_bytes(int32_t heads, int32_t dim, int32_t group, int32_t n,
                                    int32_t max_rows, int64_t max_len) {
-  if (many_rows(max_rows, group))
+  if (many_rows(dim, max_rows, group))
     return attend_tiles_partial_bytes(heads, dim, group, n, max_rows, max_len);
   const RowsPlan p = plan_rows(heads, group, n, max_rows, max_len);
   if (p.splits == 1) return 0;
@@ -519,7 +524,7 @@ size_t kv8_attention_partial_bytes(int32_t heads, int32_t dim, int32_t group, in
 }
 
 cudaError_t launch_kv8_attention(const Kv8Attention& a, cudaStream_t s) {
-  if (many_rows(a.b.max_rows, a.group)) return launch_attend_tiles(a, s);
+  if (many_rows(a.c.dim, a.b.max_rows, a.group)) return launch_attend_tiles(a, s);
   const RowsPlan p = plan_rows(a.c.heads, a.group, a.b.n, a.b.max_rows,
                                (int64_t)a.b.table_pages * a.c.page_tokens);
   if (a.c.dim == 128)

@@ -6,18 +6,37 @@
 //   warps 0..7    softmax, one thread per row (tensor-memory lane): warps 0..3
 //                 the first half, 4..7 the second.  They first bring their q
 //                 row to fp16 (a power of two out, exact) in shared memory.
-//   warps 8..11   bring K and V: 16-byte loads from the pages, E4M3 to fp16
-//                 (exact, one conversion per pair), into a ring of 128-key
-//                 tiles in the 128-byte swizzle.  The next step's loads are in
-//                 flight in registers, of K and of V apart.
-//   warp 12       allocates tensor memory; one thread issues the MMAs
+//   warps 8, 9    bring the codes of a 128-key tile to fp16 (exact, one
+//                 conversion per pair), in the 128-byte swizzle, into a ring of
+//                 four tiles.
+//   warp 10       allocates tensor memory and issues the MMAs
 //                 (tcgen05.mma.cta_group::1.kind::f16): S = Q K^T from shared
 //                 memory, O += P V with P read from tensor memory, where the
 //                 softmax writes it in the place of S.
-// The halves alternate: while one half's scores are in the softmax the tensor
+//   warp 11       looks pages up 32 at a time, one group ahead, and keeps two
+//                 tiles of codes in flight with untiled bulk copies (a page and
+//                 head is one contiguous block).
+// The halves take turns: while one half's scores are in the softmax the tensor
 // pipe works for the other.  K tiles are K-major operands; V tiles lie the
 // same way in memory, [key][dim], and are read as an MN-major operand, so
 // nothing is transposed.
+//
+// What bounds it: the turn of one half.  Scores ready -> maximum and weights of
+// 96 keys -> their product under way while the last 32 are worked on -> the
+// last product and the next scores, two hops through an mbarrier of about 200
+// clocks each on the way: about 3600 clocks alone, 2048 of them the
+// special-function unit's when both halves' exponentials are counted, and 2048
+// the tensor pipe's for both.  Measured at 4680 x 32760 x 24 heads of 128
+// (one box, us): scores in two passes, K and V through registers 1925; codes by
+// bulk copies 1845 (loads of two paths that meet wait for their data at the
+// join, and what a warp cannot keep in registers goes to an L1 cache that the
+// shared memory has left almost nothing of: no spills in any role); one pass,
+// two turns of 64 keys 1784; 96 and 32 keys 1632.  Measured and not kept: two
+// softmax warps per row, an issuing thread per half (the halves fall into step
+// and wait together, 2300), the softmax warps issuing their own products
+// (2600), scores by 64 keys in two buffers per half (products of 64 columns
+// take as long as of 128: 1900), a quarter of the exponentials as polynomials
+// on the FMA pipe (packed fma: 3.6 clocks a warp; no change).
 //
 // Tensor memory (columns): S / P of the halves at 0 and 128, O at 256 and 384.
 #include <climits>
@@ -80,12 +99,12 @@ __device__ __forceinline__ void commit(uint32_t bar, uint32_t lead) {
       : "memory");
 }
 // Shared-memory operand of 128-byte rows in the 128-byte swizzle: 8-row groups
-// 1024 bytes apart.  K-major: `lead` unused.  MN-major: the next 64 elements
-// of the row dimension lie `lead` bytes on.
-// The low word of the descriptor (address and `lead`, in 16 bytes); the high
-// word is the same for all.
-__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t lead) {
-  return (addr >> 4) | ((lead >> 4) << 16);
+// 1024 bytes apart.  MN-major: the next 64 elements of the row dimension lie
+// `block` bytes on (K-major operands do not use it).  This is the low word of
+// the descriptor (address and `block`, in units of 16 bytes); the high word is
+// the same for all.
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t block) {
+  return (addr >> 4) | ((block >> 4) << 16);
 }
 constexpr uint32_t kOperandHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
 // kind::f16, fp16 operands (format 0), fp32 accumulator; bit 16: B is MN-major.
@@ -169,19 +188,6 @@ __device__ __forceinline__ void st_wait() {
 }
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// 16 bytes, or zeros: one predicated load, no branch (which would wait for the
-// data before the next load is issued).
-__device__ __forceinline__ uint4 load_if(const void* p, bool want) {
-  uint4 v;
-  asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %5, 0;\n"
-      "mov.b32 %0, 0; mov.b32 %1, 0; mov.b32 %2, 0; mov.b32 %3, 0;\n"
-      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4]; }"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"((int)want));
-  return v;
 }
 
 // Where a 16-byte chunk of row `row` lies in a [128][64 fp16] block.
@@ -799,6 +805,7 @@ __global__ void __launch_bounds__(256)
   join_row<kTileRows>(a, q, parts, v0, plan.splits, r, row, unit.head, lane);
 }
 
+// (The caller has checked that the tiles of all sequences fit 30 bits.)
 TilesPlan plan_tiles(int32_t heads, int32_t group, int32_t n, int32_t max_rows, int64_t max_len) {
   TilesPlan p;
   p.row_tiles = (int)(((int64_t)max_rows * group + kTileRows - 1) / kTileRows);

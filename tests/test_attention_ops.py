@@ -115,6 +115,8 @@ def test_attention_refusals():
     assert go(q_head_stride=132) == ALIGN and go(w=A + 8) == ALIGN
     assert go(w=None) == WORKSPACE and go(wb=need - 1) == WORKSPACE
     assert go(batch=_batch(n=0), q=None) == OK
+    # too many tiles of query rows
+    assert go(batch=_batch(n=60000, max_rows=1 << 29, rows=1 << 40)) == SHAPE
 
 
 def test_python_refusals():

@@ -363,7 +363,6 @@ def test_attention_heads(hq, hk):
     for nq, lens in (([1, 1], [100, 500]), ([9, 2], [200, 77]), ([150], [400])):
         attend_case(nq, lens, hq, hk, 128, 64, MASKS[0], seed=hq)
         attend_case(nq, lens, hq, hk, 64, 32, MASKS[1], seed=hq, lse=False, scale=0.37)
-    assert True
 
 
 @pytest.mark.parametrize("nq", [1, 40, 600])
@@ -388,6 +387,53 @@ def test_attention_sharp_and_far_scores(nq):
     again = nv.kv8_attention(q, c, t, i32([n]), i32([0, nq]), causal=True, lse=lse)
     assert torch.equal(out, again)
     check_sequence(out, lse, q, c, t[0], n, causal=True)
+
+
+@pytest.mark.parametrize("pt,d", [(32, 64), (64, 128), (128, 128)])
+@pytest.mark.parametrize("nq", [1, 9, 300])
+def test_attention_single_keys_that_rise(pt, d, nq):
+    """One key in 128 outweighs all before it by 2^20 and more, at places all over
+    the steps, so that maxima jump in every part of a step; every query sees
+    another number of them."""
+    n = 1900
+    c = filled(-(-n // pt) + 1, 1, pt, d, 35)
+    c.k_codes.zero_()
+    c.k_scales.fill_(1.0)
+    t = torch.arange(-(-n // pt), device=DEV, dtype=torch.int32)[None].contiguous()
+    codes = c.k_codes.view(torch.float8_e4m3fn)
+    for s, at in enumerate((5, 40, 70, 95, 96, 101, 127, 120, 3, 99, 64, 111, 30, 126, 97)):
+        key = 128 * s + at
+        if key < n:
+            codes[key // pt, 0, key % pt, 0] = float(16 * (s + 1))
+    q = torch.zeros((nq, 2, d), device=DEV, dtype=torch.bfloat16)
+    q[:, 0, 0] = 1.0
+    q[:, 1, 0] = torch.linspace(-1, 3, nq, device=DEV).bfloat16()
+    for mask in (dict(causal=False), dict(causal=True, window=500)):
+        lse = torch.empty((nq, 2), device=DEV)
+        out = nv.kv8_attention(q, c, t, i32([n]), i32([0, nq]), scale=1.0, lse=lse, **mask)
+        check_sequence(out, lse, q, c, t[0], n, scale=1.0, **mask)
+
+
+@pytest.mark.parametrize("nq", [3, 200])
+def test_attention_nan_keys_reach_the_queries_that_see_them(nq):
+    c = filled(8, 1, 64, 128, 36)
+    t = torch.arange(8, device=DEV, dtype=torch.int32)[None].contiguous()
+    n, at = 500, 500 - nq // 2
+    q = torch.randn((nq, 1, 128), generator=gen(37), device=DEV).bfloat16()
+    args = (t, i32([n]), i32([0, nq]))
+    clean = nv.kv8_attention(q, c, *args, causal=True)
+    c.k_codes[at // 64, 0, at % 64, 17] = 0x7F
+    out = nv.kv8_attention(q, c, *args, causal=True)
+    first = at - (n - nq)  # the first query that sees the key
+    assert out[first:].isnan().all()
+    assert torch.equal(out[:first], clean[:first])
+
+
+def test_attention_long_cache_many_rows():
+    """More steps than any ring holds, split and whole tiles in one call."""
+    attend_case([700, 130], [4100, 3000], 16, 8, 128, 64, MASKS[1], seed=81)
+    attend_case([520], [5000], 12, 12, 64, 32, MASKS[2], seed=82)
+    attend_case([1500, 900, 1], [2000, 1024, 128], 8, 8, 128, 128, MASKS[0], seed=83)
 
 
 def test_attention_nan_and_infinite_queries_stay_in_their_rows():
