@@ -171,7 +171,8 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)
 
 // ------------------------------------------------------- partial results
 // Part `i` of `kRows` rows: kRows x dim fp32 sums of w v, then, after all
-// parts, kRows pairs (m, l) each.
+// parts, kRows pairs (m, l) each.  The sums of 8 or 16 rows lie row by row; of
+// 256 rows, whose lanes hold a row each, as dim / 4 columns of kRows groups of 4.
 template <int kRows>
 __device__ __forceinline__ float* part_rows(const Kv8Attention& a, int64_t i) {
   return a.part + i * kRows * a.c.dim;
@@ -210,7 +211,8 @@ __device__ __forceinline__ void join_row(const Kv8Attention& a, const QuerySeq& 
     for (int s = 0; s < n; ++s) {
       const float g = __shfl_sync(0xFFFFFFFFu, f, s);
       if (g == 0.0f) continue;
-      const float* src = part_rows<kRows>(a, part0 + s0 + s) + r * dim + d0;
+      const float* src = part_rows<kRows>(a, part0 + s0 + s) +
+                         (kRows <= 16 ? r * dim + d0 : (d0 / 4 * kRows + r) * 4 + d0 % 4);
       if (dim == 128) {
         const float4 x = *reinterpret_cast<const float4*>(src);
         acc[0] = fmaf(x.x, g, acc[0]), acc[1] = fmaf(x.y, g, acc[1]);

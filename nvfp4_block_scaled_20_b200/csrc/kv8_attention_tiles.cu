@@ -57,6 +57,7 @@ constexpr int kInfo = 4;     // ring of a step's scales
 constexpr int kTileThreads = 12 * 32;
 constexpr int kLoadWarp = 8, kLoadWarps = 2, kMmaWarp = 10, kCopyWarp = 11;
 constexpr uint32_t kTmemCols = 512;
+constexpr int kNoPage = INT_MIN;
 // Tensor-memory columns of a half's scores (and weights) and sums.
 __host__ __device__ constexpr uint32_t col_s(int h) { return 128u * h; }
 __host__ __device__ constexpr uint32_t col_o(int h) { return 256u + 128u * h; }
@@ -195,7 +196,8 @@ __device__ __forceinline__ uint32_t chunk_at(int row, int chunk) {
   return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
-__device__ __forceinline__ void store_bf16x8(__nv_bfloat16* dst, const uint32_t* o, float f) {
+// Eight sums times f as bf16.
+__device__ __forceinline__ uint4 bf16x8(const uint32_t* o, float f) {
   uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -203,7 +205,7 @@ __device__ __forceinline__ void store_bf16x8(__nv_bfloat16* dst, const uint32_t*
                                                    __uint_as_float(o[2 * j + 1]) * f);
     w[j] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Bits 0 .. n - 1.
@@ -306,6 +308,19 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // The copying warp's look-up: the page of each lane's piece of the steps from
+  // `step` on.  The first is on the way while the others set up.
+  const int pt_log = 31 - __clz(pt);  // 5, 6 or 7
+  const int step_log = 7 - pt_log;    // pages per step, as a power of two
+  auto fetch_page = [&](int step) {
+    const int mine = step + (lane >> step_log);
+    if (mine >= s1) return kNoPage;
+    const int key = step_at(steps, mine) * kKeys + ((lane & ((1 << step_log) - 1)) << pt_log);
+    // pages past the sequence's end are not looked up
+    return key < q.len ? a.b.table[unit.seq * a.b.table_stride + (key >> pt_log)] : kNoPage;
+  };
+  int next_page = kNoPage;
+  if (warp == kCopyWarp) next_page = fetch_page(s0);
   fence_before();
   __syncthreads();
   fence_after();
@@ -316,39 +331,52 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ---------------------------------------------------------------- softmax
     const int h = warp >> 2, r = threadIdx.x & (kHalf - 1);
     if (h < halves) {
-      float crow;
+      float crow = 0.0f;
       int at;  // place of the row's query in its sequence
+      // Rows of q and out go through a warp together, kRowLanes lanes on one
+      // (16 bytes each): a thread on a row of its own would touch a line of
+      // memory per lane.
+      constexpr int kRowLanes = kDim / 8, kRowsAtOnce = 32 / kRowLanes;
+      const int chunk = lane % kRowLanes;
       {
-        // the row to fp16, a power of two out
+        // the rows to fp16, a power of two out
         const int row = row0 + h * kHalf + r;
         const bool mine = row < rows;  // the others work on zeros and store nothing
         const int i = mine ? row / a.group : i_last;
         at = q.len - q.n + i;
-        const uint4* src = reinterpret_cast<const uint4*>(
+        const __nv_bfloat16* src =
             static_cast<const __nv_bfloat16*>(a.q) + (q.first + i) * a.q_token +
-            (int64_t)(unit.head * a.group + (mine ? row - i * a.group : 0)) * a.q_head);
-        uint32_t w[kDim / 2];
+            (int64_t)(unit.head * a.group + (mine ? row - i * a.group : 0)) * a.q_head;
+        uint4 x[kRowLanes];
 #pragma unroll
-        for (int k = 0; k < kDim / 8; ++k) {
-          const uint4 x = mine ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-          w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+        for (int t = 0; t < kRowLanes; ++t) {
+          const int from = t * kRowsAtOnce + lane / kRowLanes;
+          const uint64_t p = __shfl_sync(0xFFFFFFFFu, (uint64_t)src, from);
+          const bool live = __shfl_sync(0xFFFFFFFFu, (int)mine, from);
+          x[t] = live ? __ldg(reinterpret_cast<const uint4*>(p) + chunk) : make_uint4(0, 0, 0, 0);
         }
-        uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < kDim / 2; ++k)
-          m = max(m, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
-        const int e = m ? row_exponent(__uint_as_float(m)) : 0;
-        const float down = pow2(-e);
-        crow = a.scale_log2 * pow2(e);
+        for (int t = 0; t < kRowLanes; ++t) {
+          const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+          uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < kDim / 8; ++k) {
+          for (int k = 0; k < 4; ++k)
+            m = max(m, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+#pragma unroll
+          for (int k = 1; k < kRowLanes; k <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
+          const int e = m ? row_exponent(__uint_as_float(m)) : 0;
+          const float down = pow2(-e);
           uint32_t f[4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-            f[t] = f16x2(__uint_as_float(w[4 * k + t] << 16) * down,
-                         __uint_as_float(w[4 * k + t] & 0xFFFF0000u) * down);
-          *reinterpret_cast<uint4*>(sq + h * kTile + (k >> 3) * kBlock + chunk_at(r, k & 7)) =
+          for (int k = 0; k < 4; ++k)
+            f[k] = f16x2(__uint_as_float(w[k] << 16) * down,
+                         __uint_as_float(w[k] & 0xFFFF0000u) * down);
+          const int in = (warp & 3) * 32 + t * kRowsAtOnce + lane / kRowLanes;
+          *reinterpret_cast<uint4*>(sq + h * kTile + (chunk >> 3) * kBlock + chunk_at(in, chunk & 7)) =
               make_uint4(f[0], f[1], f[2], f[3]);
+          // each lane keeps its own row's
+          const int own = __shfl_sync(0xFFFFFFFFu, e, lane % kRowsAtOnce * kRowLanes);
+          if (lane / kRowsAtOnce == t) crow = a.scale_log2 * pow2(own);
         }
         fence_async_smem();
         __syncwarp();
@@ -509,34 +537,52 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int64_t parts = (int64_t)(plan.tiles - plan.full) * plan.splits;
         part_stats<kTileRows>(a, parts, u.part)[tid] = make_float2(m, l);
       }
+      // The rows of out through the half's q tile, which its products are done
+      // with; parts of split tiles lie so that lanes write next to each other.
+      constexpr int kRowBytes = kDim * 2;
+      uint8_t* stage = sq + h * kTile + (warp & 3) * 32 * kRowBytes;
 #pragma unroll 1
       for (int c = 0; c < kDim; c += 32) {
         uint32_t o[32];
         if (ok && n_steps > 0) {
           ld32(to + c, o);
           ld_wait<32>(o);
-        } else {
+        }
+        // a row that sees nothing is zero; a NaN sum stays
+        if (!ok || n_steps == 0 || l == 0.0f) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0u;
         }
-        if (!mine) continue;
         if (u.part >= 0) {
-          float4* dst = reinterpret_cast<float4*>(part_rows<kTileRows>(a, u.part) +
-                                                  tid * kDim + c);
+          if (!mine) continue;
+          float4* dst = reinterpret_cast<float4*>(part_rows<kTileRows>(a, u.part)) + tid;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                 __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+            dst[(c / 4 + k) * kTileRows] =
+                make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                            __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
         } else {
-          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + (qs.first + i) * a.out_token +
-                               (int64_t)qh * a.out_head + c;
-          // a row that sees nothing (sum 0) is zero; a NaN sum stays
-          if (l == 0.0f) {
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0u;
+          for (int k = 0; k < 4; ++k) {
+            const int at_chunk = c / 8 + k;
+            *reinterpret_cast<uint4*>(stage + lane * kRowBytes +
+                                      ((at_chunk & ~7) | ((at_chunk ^ lane) & 7)) * 16) =
+                bf16x8(o + 8 * k, by);
           }
+        }
+      }
+      if (u.part < 0) {
+        const __nv_bfloat16* dst = static_cast<const __nv_bfloat16*>(a.out) +
+                                   (qs.first + i) * a.out_token + (int64_t)qh * a.out_head;
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) store_bf16x8(dst + 8 * k, o + 8 * k, by);
+        for (int t = 0; t < kRowLanes; ++t) {
+          const int from = t * kRowsAtOnce + lane / kRowLanes;
+          const uint64_t to_row = __shfl_sync(0xFFFFFFFFu, (uint64_t)dst, from);
+          const bool live = __shfl_sync(0xFFFFFFFFu, (int)mine, from);
+          if (live)
+            reinterpret_cast<uint4*>(to_row)[chunk] = *reinterpret_cast<const uint4*>(
+                stage + from * kRowBytes + ((chunk & ~7) | ((chunk ^ from) & 7)) * 16);
         }
       }
       if (a.lse && mine && u.part < 0)
@@ -606,32 +652,22 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------------ copies
-    const int pt_log = 31 - __clz(pt);            // 5, 6 or 7
-    const int step_log = 7 - pt_log;              // pages per step, as a power of two
-    const int pieces = 1 << step_log, group = 32 >> step_log;  // steps per look-up
+    const int pieces = 1 << step_log, group = 32 >> step_log;  // pages per step, steps per look-up
     const uint32_t piece_bytes = (uint32_t)pt * kDim;
     const Seen first = seen_by(a, q, i_first), last = seen_by(a, q, i_last);
     // Each lane holds one of the next 32 pages and its scales; the following
     // ones are on the way, the scales a step after the pages: a look-up is two
     // dependent loads from memory, longer than a step.
-    int looked = 0, page = -1, next_page = -1;
+    int looked = s0, page = kNoPage;  // kNoPage: nothing to copy
     float ks = 0.0f, vs = -1.0f, next_ks = 0.0f, next_vs = -1.0f;
-    auto fetch_pages = [&](int step) {
-      next_page = -1;
-      const int mine = step + (lane >> step_log);
-      if (mine < s1) {
-        const int key = step_at(steps, mine) * kKeys + ((lane & (pieces - 1)) << pt_log);
-        // pages past the sequence's end are not looked up
-        if (key < q.len) {
-          next_page = a.b.table[unit.seq * a.b.table_stride + (key >> pt_log)];
-          if (next_page < 0 || next_page >= a.c.pages) {
-            atomicOr(a.err, kDevErrShape);
-            next_page = -1;
-          }
-        }
+    auto check_page = [&]() {
+      if (next_page != kNoPage && (next_page < 0 || next_page >= a.c.pages)) {
+        atomicOr(a.err, kDevErrShape);
+        next_page = kNoPage;
       }
     };
     auto fetch_scales = [&]() {
+      check_page();
       next_ks = 0.0f;
       next_vs = -1.0f;
       if (next_page >= 0) {
@@ -639,17 +675,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         next_vs = a.c.scales[1][(int64_t)next_page * a.c.heads + unit.head];
       }
     };
-    fetch_pages(s0);
-    fetch_scales();
     bool ok = true;
     int n = 0;
     for (int j = 0; j < n_steps && ok; ++j) {
-      if (j == 0 || s0 + j == looked + group) {
+      if (j == 0) {
+        check_page();
+        page = next_page;
+      } else if (s0 + j == looked + group) {
         looked = s0 + j;
         page = next_page;
         ks = next_ks;
         vs = next_vs;
-        fetch_pages(looked + group);
+        next_page = fetch_page(looked + group);
       } else if (s0 + j == looked + 1) {
         fetch_scales();
       }
@@ -660,7 +697,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const int to = n % kRaw;
         ok = warp_wait(smem_addr(&sm.raw_empty[to]), ((n / kRaw) & 1) ^ 1, gave_up, a.wait_limit_ns);
         if (!ok) break;
+        const uint32_t full = smem_addr(&sm.raw_full[to]);
+        // (the bytes may be counted down before they are announced: the phase
+        // ends with the arrival below at the earliest)
+        if (mine && page >= 0)
+          bulk_copy(smem_addr(raw) + to * (kTile / 2) + (lane - base) * piece_bytes,
+                    a.c.codes[which] + ((int64_t)page * a.c.heads + unit.head) * piece_bytes,
+                    piece_bytes, full);
         if (which == 0) {
+          if (j == 0) {
+            fetch_scales();
+            ks = next_ks;
+            vs = next_vs;
+            next_page = fetch_page(looked + group);
+          }
           // the scales of the step's four groups of 32 keys
           const int from = base + ((lane & 3) * 32 >> pt_log);
           const float k1 = __shfl_sync(0xFFFFFFFFu, ks, from), v1 = __shfl_sync(0xFFFFFFFFu, vs, from);
@@ -677,14 +727,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         __syncwarp();
-        const uint32_t full = smem_addr(&sm.raw_full[to]);
         if (lane == 0) bar_expect(full, __popc(here) * piece_bytes);
-        __syncwarp();
-        if (mine && page >= 0)
-          bulk_copy(smem_addr(raw) + to * (kTile / 2) + (lane - base) * piece_bytes,
-                    a.c.codes[which] + ((int64_t)page * a.c.heads + unit.head) * piece_bytes,
-                    piece_bytes, full);
-        __syncwarp();
       }
     }
     if (!ok) {
@@ -728,8 +771,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = warp_wait(smem_addr(&sm.q_full), 0, gave_up, a.wait_limit_ns) && wait_tile(0);
         if (ok) {
           fence_after();
-          scores(0, 0);
-          if (halves == 1) commit(smem_addr(&sm.kv_empty[0]), lead);
+          for (int h = 0; h < halves; ++h) scores(h, 0);
+          commit(smem_addr(&sm.kv_empty[0]), lead);
         }
       }
       for (int j = 0; j < n_steps && ok; ++j) {
@@ -761,13 +804,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             if (h == halves - 1) commit(smem_addr(&sm.kv_empty[nk % kSlots]), lead);
           } else {
             commit(smem_addr(&sm.o_full[h]), lead);
-          }
-          if (j == 0 && h == 0 && halves == 2) {
-            // the second half starts when the first has its first weights: from
-            // then on the halves take turns, one in the softmax and one on the
-            // tensor pipe
-            scores(1, 0);
-            commit(smem_addr(&sm.kv_empty[0]), lead);
           }
         }
       }
