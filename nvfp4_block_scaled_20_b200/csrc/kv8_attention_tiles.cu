@@ -27,11 +27,15 @@
 // clocks each on the way: about 3600 clocks alone, 2048 of them the
 // special-function unit's when both halves' exponentials are counted, and 2048
 // the tensor pipe's for both.  Measured at 4680 x 32760 x 24 heads of 128
-// (one box, us): scores in two passes, K and V through registers 1925; codes by
+// (one GPU, us): scores in two passes, K and V through registers 1925; codes by
 // bulk copies 1845 (loads of two paths that meet wait for their data at the
 // join, and what a warp cannot keep in registers goes to an L1 cache that the
-// shared memory has left almost nothing of: no spills in any role); one pass,
-// two turns of 64 keys 1784; 96 and 32 keys 1632.  Measured and not kept: two
+// shared memory has left almost nothing of: spills in a step cost more than the
+// work they stand for); one pass, two turns of 64 keys 1784; 96 and 32 keys
+// 1632 while the GPU is cool, 1700 to 1800 (1050 to 1110 TFLOP/s) in a loop that
+// holds it at its power limit.  What a tile costs besides its steps, 4736 rows
+// of 24 heads that see 128 keys: 57 with a thread on each row of q and out, 45
+// with a warp on each row.  Measured and not kept: two
 // softmax warps per row, an issuing thread per half (the halves fall into step
 // and wait together, 2300), the softmax warps issuing their own products
 // (2600), scores by 64 keys in two buffers per half (products of 64 columns
@@ -347,36 +351,41 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const __nv_bfloat16* src =
             static_cast<const __nv_bfloat16*>(a.q) + (q.first + i) * a.q_token +
             (int64_t)(unit.head * a.group + (mine ? row - i * a.group : 0)) * a.q_head;
-        uint4 x[kRowLanes];
+        constexpr int kAtOnce = 8;  // loads in flight; 16 spill: 419 us for 3 prompts, 405 so
+#pragma unroll 1
+        for (int t0 = 0; t0 < kRowLanes; t0 += kAtOnce) {
+          uint4 x[kAtOnce];
 #pragma unroll
-        for (int t = 0; t < kRowLanes; ++t) {
-          const int from = t * kRowsAtOnce + lane / kRowLanes;
-          const uint64_t p = __shfl_sync(0xFFFFFFFFu, (uint64_t)src, from);
-          const bool live = __shfl_sync(0xFFFFFFFFu, (int)mine, from);
-          x[t] = live ? __ldg(reinterpret_cast<const uint4*>(p) + chunk) : make_uint4(0, 0, 0, 0);
-        }
+          for (int t = 0; t < kAtOnce; ++t) {
+            const int from = (t0 + t) * kRowsAtOnce + lane / kRowLanes;
+            const uint64_t p = __shfl_sync(0xFFFFFFFFu, (uint64_t)src, from);
+            const bool live = __shfl_sync(0xFFFFFFFFu, (int)mine, from);
+            x[t] = live ? __ldg(reinterpret_cast<const uint4*>(p) + chunk) : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-        for (int t = 0; t < kRowLanes; ++t) {
-          const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
-          uint32_t m = 0;
+          for (int t = 0; t < kAtOnce; ++t) {
+            const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+            uint32_t m = 0;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            m = max(m, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
+            for (int k = 0; k < 4; ++k)
+              m = max(m, max((w[k] << 16) & 0x7FFFFFFFu, w[k] & 0x7FFF0000u));
 #pragma unroll
-          for (int k = 1; k < kRowLanes; k <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
-          const int e = m ? row_exponent(__uint_as_float(m)) : 0;
-          const float down = pow2(-e);
-          uint32_t f[4];
+            for (int k = 1; k < kRowLanes; k <<= 1)
+              m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, k));
+            const int e = m ? row_exponent(__uint_as_float(m)) : 0;
+            const float down = pow2(-e);
+            uint32_t f[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            f[k] = f16x2(__uint_as_float(w[k] << 16) * down,
-                         __uint_as_float(w[k] & 0xFFFF0000u) * down);
-          const int in = (warp & 3) * 32 + t * kRowsAtOnce + lane / kRowLanes;
-          *reinterpret_cast<uint4*>(sq + h * kTile + (chunk >> 3) * kBlock + chunk_at(in, chunk & 7)) =
-              make_uint4(f[0], f[1], f[2], f[3]);
-          // each lane keeps its own row's
-          const int own = __shfl_sync(0xFFFFFFFFu, e, lane % kRowsAtOnce * kRowLanes);
-          if (lane / kRowsAtOnce == t) crow = a.scale_log2 * pow2(own);
+            for (int k = 0; k < 4; ++k)
+              f[k] = f16x2(__uint_as_float(w[k] << 16) * down,
+                           __uint_as_float(w[k] & 0xFFFF0000u) * down);
+            const int in = (warp & 3) * 32 + (t0 + t) * kRowsAtOnce + lane / kRowLanes;
+            *reinterpret_cast<uint4*>(sq + h * kTile + (chunk >> 3) * kBlock +
+                                      chunk_at(in, chunk & 7)) = make_uint4(f[0], f[1], f[2], f[3]);
+            // each lane keeps its own row's
+            const int own = __shfl_sync(0xFFFFFFFFu, e, lane % kRowsAtOnce * kRowLanes);
+            if (lane / kRowsAtOnce == t0 + t) crow = a.scale_log2 * pow2(own);
+          }
         }
         fence_async_smem();
         __syncwarp();
