@@ -24,10 +24,11 @@ _QUERY = struct.Struct("@PPPi4xqqqqfiii")       # nvfp4_kv8_query
 _ROPE_TENSORS = [struct.Struct("@" + _ROPE_TENSOR * n) for n in range(9)]
 
 
-@dataclass
+@dataclass(frozen=True)
 class KV8Cache:
     """A paged KV cache in E4M3: codes uint8 [pages, heads, page_tokens,
-    head_dim], one fp32 power-of-two scale per page and head [pages, heads]."""
+    head_dim], one fp32 power-of-two scale per page and head [pages, heads].
+    Its tensors stay the ones that it was made of."""
     k_codes: object
     v_codes: object
     k_scales: object
@@ -46,11 +47,11 @@ class KV8Cache:
                 raise ValueError("scales are contiguous fp32 [pages, heads] tensors")
         if any(t.device != k.device for t in (self.v_codes, self.k_scales, self.v_scales)):
             raise ValueError("a cache lives on one device")
-        self.heads, self.page_tokens, self.head_dim = k.shape[1:]
-        self.device, self.index = k.device, k.get_device()
-        self.desc = bytes(capi.nvfp4_kv8_cache(
-            k.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
-            self.v_scales.data_ptr(), *k.shape))
+        vars(self).update(
+            heads=k.shape[1], page_tokens=k.shape[2], head_dim=k.shape[3], device=k.device,
+            index=k.get_device(), desc=bytes(capi.nvfp4_kv8_cache(
+                k.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
+                self.v_scales.data_ptr(), *k.shape)))
 
 
 def kv8_cache(pages, heads, page_tokens=64, head_dim=128, device=None):
@@ -106,6 +107,12 @@ def _packed(x, rows, cache, what):
     return t, h
 
 
+def _workspace(ws, cache):
+    if ws.get_device() != cache.index or not ws.is_contiguous():
+        raise ValueError("the workspace is contiguous and on the cache's device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _batch(cache, page_table, lens, starts, rows, max_rows):
     i32 = _torch().int32
     if not (page_table.dtype is i32 and lens.dtype is i32 and starts.dtype is i32):
@@ -119,9 +126,11 @@ def _batch(cache, page_table, lens, starts, rows, max_rows):
         raise ValueError("page_table is [n, pages], lens [n], starts [n + 1]")
     stride, one = page_table.stride()
     width = page_table.shape[1]
+    if stride < width and n > 1:
+        raise ValueError("page_table's rows overlap")
     if (one != 1 and width > 1) or not lens.is_contiguous() or not starts.is_contiguous():
         raise ValueError("page_table's rows, lens and starts are contiguous")
-    return _BATCH.pack(page_table.data_ptr(), stride if stride > width else width, width,
+    return _BATCH.pack(page_table.data_ptr(), stride if n > 1 else width, width,
                        lens.data_ptr(), starts.data_ptr(), n, rows, max_rows)
 
 
@@ -136,6 +145,8 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
         raise ValueError("rope takes 1 to 8 tensors and 1 to 4 sections")
     if outs is None:
         outs = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs]
+    elif len(outs) != n:
+        raise ValueError("rope has one output per tensor")
     first = xs[0]
     if first.dim() != 3:
         raise ValueError("rope's tensors are [tokens, heads, head_dim]")
@@ -147,6 +158,10 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     stride, one = positions.stride()
     if one != 1 and positions.shape[1] > 1:
         raise ValueError("positions' rows are contiguous")
+    if tokens < 2:
+        stride = axes
+    elif stride < axes:
+        raise ValueError("positions' rows overlap")
     fields = []
     for x, o in zip(xs, outs):
         if x.dim() != 3 or o.shape != x.shape or x.shape[0] != tokens or x.shape[2] != dim:
@@ -163,7 +178,7 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     rp = _ROPE_PARAMS.pack(axes, *sections, *pad[axes:], theta, bool(interleaved), bool(per_axis),
                            bool(inverse))
     _call("nvfp4_rope", at, stream, _ROPE_TENSORS[n].pack(*fields), n, _type(first), tokens, dim,
-          positions.data_ptr(), stride if stride > axes else axes, rp)
+          positions.data_ptr(), stride, rp)
     return outs
 
 
@@ -179,7 +194,7 @@ def kv8_write(cache, k, v, page_table, lens, starts, max_new=None, ws=None, stre
     b = _batch(cache, page_table, lens, starts, rows, rows if max_new is None else max_new)
     ws = workspace(0, cache.device) if ws is None else ws
     _call("nvfp4_kv8_write", cache.index, stream, cache.desc, b, _type(k), k.data_ptr(), kt, kh,
-          v.data_ptr(), vt, vh, ws.data_ptr(), ws.numel())
+          v.data_ptr(), vt, vh, *_workspace(ws, cache))
 
 
 def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype=None, outs=None,
@@ -199,7 +214,7 @@ def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype
     b = _batch(cache, page_table, begins, starts, rows, rows if max_tokens is None else max_tokens)
     ws = workspace(0, cache.device) if ws is None else ws
     _call("nvfp4_kv8_read", cache.index, stream, cache.desc, b, _type(k), k.data_ptr(), kt, kh,
-          v.data_ptr(), vt, vh, ws.data_ptr(), ws.numel())
+          v.data_ptr(), vt, vh, *_workspace(ws, cache))
     return outs
 
 
@@ -248,6 +263,5 @@ def kv8_attention(q, cache, page_table, lens, starts, max_q=None, scale=None, ca
         scale = 1.0 / math.sqrt(cache.head_dim)
     query = _QUERY.pack(q.data_ptr(), out.data_ptr(), at, q_heads, qt, qh, ot, oh, scale,
                         bool(causal), window, sink)
-    _call("nvfp4_kv8_attention", cache.index, stream, cache.desc, b, query, ws.data_ptr(),
-          ws.numel())
+    _call("nvfp4_kv8_attention", cache.index, stream, cache.desc, b, query, *_workspace(ws, cache))
     return out

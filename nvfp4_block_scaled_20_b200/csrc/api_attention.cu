@@ -167,9 +167,12 @@ nvfp4_status nvfp4_kv8_read(const nvfp4_kv8_cache* cache, const nvfp4_kv8_batch*
 
 namespace {
 // Tiles of query rows over all sequences and KV heads, each a CTA or several:
-// at most 2^30.
+// at most 2^30.  Of up to three tiles of 16 rows, tiles and heads are a grid
+// dimension.
 inline bool tiles_ok(int64_t heads, int64_t group, int64_t n, int64_t max_rows) {
-  return max_rows * group <= (1 << 30) && (max_rows * group + 255) / 256 * heads * n <= (1 << 30);
+  const int64_t rows = max_rows * group;
+  return rows <= (1 << 30) && (rows + 255) / 256 * heads * n <= (1 << 30) &&
+         (rows > 48 || (rows + 15) / 16 * heads <= 65535);
 }
 }  // namespace
 
@@ -177,7 +180,7 @@ size_t nvfp4_kv8_attention_workspace_bytes(int32_t heads, int32_t head_dim, int3
                                            int32_t q_heads, int32_t n, int32_t max_rows,
                                            int32_t table_pages) {
   if (heads < 1 || q_heads < heads || q_heads % heads || n < 1 || max_rows < 1 || table_pages < 1 ||
-      page_tokens < 1 || head_dim < 1 || !tiles_ok(heads, q_heads / heads, n, max_rows))
+      page_tokens < 1 || (head_dim != 64 && head_dim != 128) || !tiles_ok(heads, q_heads / heads, n, max_rows))
     return kPartOffset;
   return kPartOffset + kv8_attention_partial_bytes(heads, head_dim, q_heads / heads, n, max_rows,
                                                    (int64_t)table_pages * page_tokens);

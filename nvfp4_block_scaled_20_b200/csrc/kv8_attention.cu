@@ -658,12 +658,14 @@ cudaError_t launch_rows(const Kv8Attention& a, const RowsPlan& p, cudaStream_t s
 
 namespace {
 // Whether tiles of 256 rows on the tensor pipe are faster than tiles of 16 rows
-// that each read the cache.  Measured at 8 sequences of 4100..8200 tokens, 4 KV
-// heads (tiles of 256 / of 16 rows, us): dim 128, 24 rows 42 / 52, 48 rows 43 /
-// 67; dim 64, 24 rows 37 / 25, 48 rows 37 / 32, 66 rows 38 / 61.  So above one
-// tile of 16 rows at 128 and above two at 64.
+// that each read the cache.  Measured with rows of 6 heads (tiles of 256 / of 16
+// rows, us): 8 sequences of 4100..8200 tokens and 4 KV heads, dim 64, 30 rows
+// 38 / 22, 48 rows 38 / 32, 66 rows 38 / 54; dim 128, 30 rows 44 / 41, 48 rows
+// 44 / 58.  32 sequences and 8 KV heads: dim 64, 48 rows 192 / 176, 66 rows 192
+// / 268; dim 128, 30 rows 213 / 217, 48 rows 214 / 311.  So above three tiles of
+// 16 rows at 64 and above two at 128.
 inline bool many_rows(int32_t dim, int64_t max_rows, int32_t group) {
-  return max_rows * group * dim > 2048;
+  return max_rows * group > 16 * (dim == 64 ? 3 : 2);
 }
 }  // namespace
 

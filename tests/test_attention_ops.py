@@ -151,6 +151,43 @@ def test_workspace_grows_with_the_split():
     assert f(8, 128, 64, 8, 1, 1, 512) > f(8, 128, 64, 8, 1, 1, 8) > base
 
 
+def test_workspace_of_sizes_that_a_call_refuses():
+    base = capi.nvfp4_workspace_bytes(0)
+    f = capi.nvfp4_kv8_attention_workspace_bytes
+    for bad in ((0, 128, 64, 8, 1, 1, 4), (8, 256, 64, 8, 1, 1, 4), (8, 0, 64, 8, 1, 1, 4),
+                (8, 96, 64, 8, 1, 1, 4), (8, 128, 0, 8, 1, 1, 4), (8, 128, 64, 12, 1, 1, 4),
+                (8, 128, 64, 8, 0, 1, 4), (8, 128, 64, 8, 1, 1, 0), (32767, 64, 64, 32767, 1, 33, 4)):
+        assert f(*bad) == base, bad
+    # more tiles and heads than a grid dimension holds
+    need = 1 << 30
+    query = dict(q=A, out=A, lse=None, q_heads=32767, q_token_stride=32767 * 64, q_head_stride=64,
+                 out_token_stride=32767 * 64, out_head_stride=64, scale=0.1, causal=1, window=-1,
+                 sink=0)
+    assert capi.nvfp4_kv8_attention(_cache(heads=32767, head_dim=64), _batch(max_rows=33, rows=66),
+                                    capi.nvfp4_kv8_query(**query), A, need, None) == SHAPE
+
+
+def test_python_refuses_rows_that_overlap_and_workspaces_elsewhere():
+    import nvfp4_block_scaled_20_b200 as nv
+    c = nv.kv8_cache(4, 2, 32, 64, device="cpu")
+    lens, starts = torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    k = torch.zeros(3, 2, 64)
+    t = torch.zeros((1, 2), dtype=torch.int32).expand(2, 2)
+    with pytest.raises(ValueError, match="overlap"):
+        nv.kv8_write(c, k, k, t, lens, starts, ws=starts)
+    with pytest.raises(ValueError, match="overlap"):
+        nv.kv8_attention(k.bfloat16(), c, t, lens, starts, ws=starts)
+    with pytest.raises(ValueError, match="overlap"):
+        nv.rope([k], torch.zeros((1, 2), dtype=torch.int32).expand(3, 2), [4, 4])
+    with pytest.raises(ValueError, match="one output"):
+        nv.rope([k], torch.zeros((3, 2), dtype=torch.int32), [4, 4], outs=[k, k])
+    with pytest.raises(ValueError, match="workspace"):
+        nv.kv8_write(c, k, k, t.contiguous(), lens, starts,
+                     ws=torch.zeros((8, 8), dtype=torch.uint8).t())
+    with pytest.raises(AttributeError):
+        c.k_codes = c.v_codes
+
+
 # ------------------------------------------------------- the plain forms
 def test_plain_e4m3_is_the_nearest_value():
     grid = torch.arange(0, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()

@@ -436,6 +436,29 @@ def test_attention_long_cache_many_rows():
     attend_case([1500, 900, 1], [2000, 1024, 128], 8, 8, 128, 128, MASKS[0], seed=83)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,lens,hk", [
+    ([1, 2], [9000, 130], 2),                       # many even shares
+    ([2, 0, 1], [700, 65, 3], 2),                   # few of them
+    ([1] * 40, [4200] + list(range(60, 99)), 8)])   # runs of fixed length
+@pytest.mark.parametrize("mask", [0, 2])
+def test_attention_few_rows_however_they_are_split(nq, lens, hk, d, mask):
+    """Also where the page table is far wider than the sequences, with entries
+    past them that name no page."""
+    c, q, t, ln, starts, ws, out, ls = attend_case(nq, lens, 2 * hk, hk, d, 64, MASKS[mask], seed=91)
+    wide = torch.full((t.shape[0], 420), c.k_codes.shape[0], dtype=torch.int32, device=DEV)
+    wide[:, :t.shape[1]] = t
+    w2 = nv.kv8_attention_workspace(c, wide, starts, 2 * hk, max(nq))
+    other, l2 = torch.full_like(out, 9.0), torch.full_like(ls, 9.0)
+    for _ in range(2):  # the same workspace twice
+        nv.kv8_attention(q, c, wide, ln, starts, max_q=max(nq), out=other, lse=l2, ws=w2, **MASKS[mask])
+        assert nv.device_error(w2) == 0
+        for s, n in enumerate(lens):
+            a, b = sum(nq[:s]), sum(nq[:s + 1])
+            check_sequence(other[a:b], l2[a:b], q[a:b], c, t[s], n, **MASKS[mask])
+        assert (other[sum(nq):] == 9.0).all() and (l2[sum(nq):] == 9.0).all()
+
+
 def test_attention_nan_and_infinite_queries_stay_in_their_rows():
     c = filled(4, 1, 64, 64, 41)
     q = torch.randn((4, 2, 64), generator=gen(42), device=DEV).bfloat16()
