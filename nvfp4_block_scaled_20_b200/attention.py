@@ -143,7 +143,8 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     n, axes = len(xs), len(sections)
     if not 1 <= n <= 8 or not 1 <= axes <= 4:
         raise ValueError("rope takes 1 to 8 tensors and 1 to 4 sections")
-    if outs is None:
+    given = outs is not None
+    if not given:
         outs = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs]
     elif len(outs) != n:
         raise ValueError("rope has one output per tensor")
@@ -164,16 +165,23 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
         raise ValueError("positions' rows overlap")
     fields = []
     for x, o in zip(xs, outs):
-        if x.dim() != 3 or o.shape != x.shape or x.shape[0] != tokens or x.shape[2] != dim:
+        shape = x.shape
+        if len(shape) != 3 or shape[0] != tokens or shape[2] != dim:
             raise ValueError("rope's tensors are [tokens, heads, head_dim] of one token count")
-        if x.dtype is not kind or o.dtype is not kind or x.get_device() != at or (
-                o.get_device() != at):
+        if x.dtype is not kind or x.get_device() != at:
             raise ValueError("rope's tensors are of one type and device")
+        heads = shape[1]
         xt, xh, xe = x.stride()
-        ot, oh, oe = o.stride()
+        ot, oh, oe = heads * dim, dim, 1
+        if given:
+            if o.shape != shape:
+                raise ValueError("rope's tensors are [tokens, heads, head_dim] of one token count")
+            if o.dtype is not kind or o.get_device() != at:
+                raise ValueError("rope's tensors are of one type and device")
+            ot, oh, oe = o.stride()
         if (xe != 1 or oe != 1) and dim > 1:
             raise ValueError("rope: the elements of a head are not contiguous")
-        fields += (x.data_ptr(), o.data_ptr(), x.shape[1], xt, xh, ot, oh)
+        fields += (x.data_ptr(), o.data_ptr(), heads, xt, xh, ot, oh)
     pad = (0, 0, 0, 0)
     rp = _ROPE_PARAMS.pack(axes, *sections, *pad[axes:], theta, bool(interleaved), bool(per_axis),
                            bool(inverse))
@@ -203,14 +211,17 @@ def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype
     starts[s]..starts[s+1] of the returned (k, v), [rows, heads, head_dim]."""
     torch = _torch()
     if outs is None:
-        out = torch.empty((2, rows, cache.heads, cache.head_dim), device=cache.device,
-                          dtype=torch.bfloat16 if out_dtype is None else out_dtype)
-        outs = out[0], out[1]
-    k, v = outs
-    kt, kh = _packed(k, rows, cache, "k")
-    vt, vh = _packed(v, rows, cache, "v")
-    if k.shape[1] != cache.heads or v.shape[1] != cache.heads or v.dtype is not k.dtype:
-        raise ValueError("k and v have the cache's heads and one type")
+        shape, kind = (rows, cache.heads, cache.head_dim), out_dtype or torch.bfloat16
+        outs = k, v = (torch.empty(shape, device=cache.device, dtype=kind),
+                       torch.empty(shape, device=cache.device, dtype=kind))
+        kh = vh = cache.head_dim
+        kt = vt = cache.heads * kh
+    else:
+        k, v = outs
+        kt, kh = _packed(k, rows, cache, "k")
+        vt, vh = _packed(v, rows, cache, "v")
+        if k.shape[1] != cache.heads or v.shape[1] != cache.heads or v.dtype is not k.dtype:
+            raise ValueError("k and v have the cache's heads and one type")
     b = _batch(cache, page_table, begins, starts, rows, rows if max_tokens is None else max_tokens)
     ws = workspace(0, cache.device) if ws is None else ws
     _call("nvfp4_kv8_read", cache.index, stream, cache.desc, b, _type(k), k.data_ptr(), kt, kh,
