@@ -545,7 +545,10 @@ typedef struct nvfp4_kv8_query {
  * Workspace: nvfp4_kv8_attention_workspace_bytes, 16-byte aligned (the error
  * word, zero at first, and partial results of key ranges, joined in the order
  * of the keys: the result is deterministic).  One call in flight per
- * workspace. */
+ * workspace.
+ * Sizes: at most 2^30 tiles of 256 rows (queries times q_heads / heads) over all
+ * sequences and KV heads, and for at most 48 rows a sequence at most 65535 KV
+ * heads times tiles of 16 rows.  Waits are bounded (nvfp4_set_wait_limit). */
 NVFP4_API nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache,
                                            const nvfp4_kv8_batch* batch,
                                            const nvfp4_kv8_query* query, void* workspace,
@@ -587,8 +590,9 @@ NVFP4_API nvfp4_status nvfp4_rht16(const void* x, int32_t dtype, int64_t rows,
 NVFP4_API nvfp4_status nvfp4_convert_sweep(int32_t target, uint32_t first_bits, int64_t count,
                                            uint8_t* out, void* stream);
 
-/* Bound, in nanoseconds, of every wait in nvfp4_gemm's pipeline (0 restores
- * the default, 2 s), for the whole process, read at each nvfp4_gemm call.
+/* Bound, in nanoseconds, of every wait in the pipelines of nvfp4_gemm and
+ * nvfp4_kv8_attention (0 restores the default, 2 s), for the whole process, read
+ * at each of their calls.
  * A wait that runs out records NVFP4_ERR_TIMEOUT in the workspace error
  * word; the kernel then waits (with bounds of its own, independent of this
  * one) for the copies and MMAs it issued, frees its tensor memory and

@@ -40,7 +40,12 @@
 // and wait together, 2300), the softmax warps issuing their own products
 // (2600), scores by 64 keys in two buffers per half (products of 64 columns
 // take as long as of 128: 1900), a quarter of the exponentials as polynomials
-// on the FMA pipe (packed fma: 3.6 clocks a warp; no change).
+// on the FMA pipe (packed fma: 3.6 clocks a warp; no change), CTAs that stay and
+// take the next tile by cluster launch control (they hide a tile's set-up and
+// look-ups, 0.5 us of 9, and cost registers in the steps: three prompts 439 for
+// 405, a chunk 1820 for 1720), counting the tiles of ragged sequences in the
+// kernel to split the true last round (three prompts 399 for 405, one prompt
+// 224 for 217, 40 short ones 1122 for 1095).
 //
 // Tensor memory (columns): S / P of the halves at 0 and 128, O at 256 and 384.
 #include <climits>
