@@ -504,6 +504,51 @@ def test_attention_strided_and_on_another_stream():
     assert (out[:, :4] == 3.0).all() and (out[:, 8:] == 3.0).all()
 
 
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_shared_pages_two_streams_and_replays(nq):
+    """Sequences that share prefix pages, one of them the same page twice; two
+    calls at once on their own workspaces; a captured call replayed with other
+    lengths, some of them zero."""
+    hk, hq, d, pt = 2, 6, 128, 64
+    c = filled(12, hk, pt, d, 101)
+    t = i32([[3, 1, 4, 0, 5, 9, 2, 6], [3, 1, 4, 8, 7, 7, 7, 10], [3, 1, 11, 11, 0, 0, 0, 0]])
+    starts = i32([0, nq, 2 * nq, 3 * nq])
+    q = (torch.randn((3 * nq, hq, d), generator=gen(102), device=DEV) * 0.1).bfloat16()
+
+    def check(out, lens):
+        for s, n in enumerate(lens):
+            check_sequence(out[s * nq:(s + 1) * nq], None, q[s * nq:(s + 1) * nq], c, t[s], n, causal=True)
+
+    first, second = [512, 500, 190], [70, 0, 256]
+    want = []
+    for lens in (first, second):
+        want.append(nv.kv8_attention(q, c, t, i32(lens), starts, max_q=nq, causal=True))
+        check(want[-1], lens)
+    # two at once, each on its stream
+    streams = [torch.cuda.Stream() for _ in "ab"]
+    ws = [nv.kv8_attention_workspace(c, t, starts, hq, nq) for _ in "ab"]
+    lens = [i32(first), i32(second)]
+    outs = [[torch.empty_like(q) for _ in range(20)] for _ in "ab"]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for i in range(2):
+            nv.kv8_attention(q, c, t, lens[i], starts, max_q=nq, causal=True, out=outs[i][k],
+                             ws=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+    # captured once
+    n, out = i32(first), torch.empty_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        nv.kv8_attention(q, c, t, n, starts, max_q=nq, causal=True, out=out, ws=ws[0])
+    for i in (1, 0, 1):
+        n.copy_(lens[i])
+        graph.replay()
+        assert torch.equal(out, want[i])
+    assert nv.device_error(ws[0]) == 0 and nv.device_error(ws[1]) == 0
+
+
 def test_offsets_past_32_bits():
     """Pages whose bytes lie past 2^32 of a long cache."""
     heads, pt, d = 16, 128, 128
