@@ -406,16 +406,21 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(kDim, kTiles))
           const uint2 x = *reinterpret_cast<const uint2*>(vr);
           v[u][k][0] = x.x, v[u][k][1] = x.y;
         }
-        // codes that no row sees, past the sequence's end above all, may be
-        // anything, NaN among it, and 0 * NaN is not 0
-        if (!whole) {
-          const int key = key0 + in;
+      }
+    // codes that no row sees, past the sequence's end above all, may be
+    // anything, NaN among it, and 0 * NaN is not 0
+    if (!whole) {
+#pragma unroll
+      for (int u = 0; u < kGroups; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int key = key0 + 16 * u + 2 * c + (k & 1) + 8 * (k >> 1);
           if (absent || !((key >= first.lo && key < last.hi) || key < last.sink)) {
 #pragma unroll
             for (int w = 0; w < kVWords; ++w) v[u][k][w] = 0u;
           }
         }
-      }
+    }
     // the step's bytes are in registers: its slot may refill
     __syncwarp();
     if (lane == 0) bar_arrive(smem_addr(&sm.empty[st]));
@@ -434,13 +439,34 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(kDim, kTiles))
           for (int j = 0; j < 2; ++j) {
             float& x = s[u][n][2 * j + h];
             x = fmaf(x, f, lv);
-            if (!all_see) {
-              const Seen see = seen_at(a, q.len, at[n][h]);
-              const int key = key0 + 16 * u + g + 8 * j;
-              if (absent || !((key >= see.lo && key < see.hi) || key < see.sink)) x = kNegInf;
-            }
-            higher |= x > m[n][h] + kLazy;
           }
+      }
+    if (!all_see) {
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const Seen see = seen_at(a, q.len, at[n][h]);
+#pragma unroll
+          for (int u = 0; u < kGroups; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int key = key0 + 16 * u + g + 8 * j;
+              if (absent || !((key >= see.lo && key < see.hi) || key < see.sink))
+                s[u][n][2 * j + h] = kNegInf;
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float top = s[0][n][h];
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) top = fmaxf(top, s[u][n][2 * j + h]);
+        higher |= top > m[n][h] + kLazy;
       }
     if (__any_sync(0xFFFFFFFFu, higher)) {
 #pragma unroll
