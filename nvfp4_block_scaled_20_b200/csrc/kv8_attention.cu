@@ -29,16 +29,17 @@
 //     eight short runs are one cluster, which joins its sums through distributed
 //     shared memory; more or longer ones are joined by a second kernel.  One
 //     token of 24 heads of 128, us with the cluster / the kernel: 1561 tokens
-//     9.1 / 11.3, 3000 10.6 / 12.5, 6000 15.8 / 16.6, 12000 (24 steps a run)
-//     24.5 / 23.5.
+//     8.8 / 11.3, 3000 10.1 / 12.3, 6000 15.2 / 16.6, 12000 (24 steps a run)
+//     23.5 / 23.4.
 //   * Beyond: runs of fixed length; those past a sequence's end return at once.
 //     Even shares there start more CTAs for the same work (32 sequences, 8 heads
 //     of 128: 193 us in shares of at least 16 steps, 184 in runs of 64).
 // Measured (device time): 32 sequences of 800..32760 tokens, 8 KV heads of 128,
-// 4 query heads each: 184 us, 6.0 TB/s.  8 sequences of 4100..8200 tokens, 4 KV
-// heads of 64, 30 rows each: 22 us, of which the bytes are 4: instructions
-// (about 250 per 16 keys and warp, conversions and softmax above all); with 64
-// keys a step 25, with 32 rows a CTA (half the conversions, two CTAs an SM) 31.
+// 4 query heads each: 183 us, 6.0 TB/s.  8 sequences of 4100..8200 tokens, 4 KV
+// heads of 64, 30 rows each: 19.7 us, of which the bytes are 4: a warp's chain
+// of conversions, products and softmax, three CTAs an SM.  With 64 keys a step 3
+// us more, with a branch per masked key or 32 rows a CTA (half the conversions,
+// two CTAs an SM) 3 and 9 more.
 #include "attention_common.cuh"
 #include "kernels.h"
 
@@ -686,9 +687,9 @@ namespace {
 // Whether tiles of 256 rows on the tensor pipe are faster than tiles of 16 rows
 // that each read the cache.  Measured with rows of 6 heads (tiles of 256 / of 16
 // rows, us): 8 sequences of 4100..8200 tokens and 4 KV heads, dim 64, 30 rows
-// 38 / 22, 48 rows 38 / 32, 66 rows 38 / 54; dim 128, 30 rows 44 / 41, 48 rows
-// 44 / 58.  32 sequences and 8 KV heads: dim 64, 48 rows 192 / 176, 66 rows 192
-// / 268; dim 128, 30 rows 213 / 217, 48 rows 214 / 311.  So above three tiles of
+// 38 / 20, 48 rows 38 / 28, 66 rows 38 / 46; dim 128, 30 rows 44 / 37, 48 rows
+// 44 / 51.  32 sequences and 8 KV heads: dim 64, 48 rows 191 / 145, 66 rows 192
+// / 221; dim 128, 30 rows 214 / 191, 48 rows 215 / 272.  So above three tiles of
 // 16 rows at 64 and above two at 128.
 inline bool many_rows(int32_t dim, int64_t max_rows, int32_t group) {
   return max_rows * group > 16 * (dim == 64 ? 3 : 2);
