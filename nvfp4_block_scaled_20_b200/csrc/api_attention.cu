@@ -234,7 +234,6 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
   if (!aligned(ws, 16)) return NVFP4_ERR_ALIGN;
   a.err = static_cast<uint32_t*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPartOffset);
-  a.part_bytes = ws_bytes - kPartOffset;
   a.wait_limit_ns = gemm_wait_limit_ns();
   return cuda_status(launch_kv8_attention(a, S(stream)));
 }

@@ -76,7 +76,6 @@ struct Kv8Attention {
   int32_t causal, window, sink;
   uint32_t* err;
   float* part;  // partial results of split tiles (workspace)
-  size_t part_bytes;
   uint64_t wait_limit_ns;
 };
 // Bytes of partial results the launch of these sizes uses.
