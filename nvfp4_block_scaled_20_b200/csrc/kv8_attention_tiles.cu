@@ -34,7 +34,7 @@
 // work they stand for); one pass, two turns of 64 keys 1784; 96 and 32 keys
 // 1632 while the GPU is cool, 1700 to 1800 (1050 to 1110 TFLOP/s) in a loop that
 // holds it at its power limit.  What a tile costs besides its steps, 4736 rows
-// of 24 heads that see 128 keys: 57 with a thread on each row of q and out, 45
+// of 24 heads that see 128 keys: 57 with a thread on each row of q and out, 44
 // with a warp on each row.  Measured and not kept: two
 // softmax warps per row, an issuing thread per half (the halves fall into step
 // and wait together, 2300), the softmax warps issuing their own products
@@ -330,6 +330,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   };
   int next_page = kNoPage;
   if (warp == kCopyWarp) next_page = fetch_page(s0);
+  if (threadIdx.x < kTileRows && row0 + (int)threadIdx.x < rows) {
+    // and so are the rows of q, as far as the L2 cache (a tile of one step: 2 of
+    // 46 us of four rounds)
+    const int row = row0 + threadIdx.x, i = row / a.group;
+    const char* src = reinterpret_cast<const char*>(
+        static_cast<const __nv_bfloat16*>(a.q) + (q.first + i) * a.q_token +
+        (int64_t)(unit.head * a.group + row - i * a.group) * a.q_head);
+#pragma unroll
+    for (int k = 0; k < kDim * 2; k += 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(src + k));
+  }
   fence_before();
   __syncthreads();
   fence_after();
