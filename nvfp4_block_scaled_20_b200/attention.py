@@ -15,13 +15,20 @@ import math
 import struct
 from dataclasses import dataclass
 
-from . import NVFP4_BF16, NVFP4_F32, _torch, capi, workspace
+from . import NVFP4_BF16, NVFP4_F32, capi, workspace
+
+torch = None  # from the first call on: the package can be imported without it
 
 _ROPE_TENSOR = "PPqqqqq"                        # nvfp4_rope_tensor
 _ROPE_PARAMS = struct.Struct("@5id3i4x")        # nvfp4_rope_params
 _BATCH = struct.Struct("@Pqi4xPPi4xqi4x")       # nvfp4_kv8_batch
 _QUERY = struct.Struct("@PPPi4xqqqqfiii")       # nvfp4_kv8_query
 _ROPE_TENSORS = [struct.Struct("@" + _ROPE_TENSOR * n) for n in range(9)]
+
+
+def _need_torch():
+    global torch
+    import torch
 
 
 @dataclass(frozen=True)
@@ -35,7 +42,7 @@ class KV8Cache:
     v_scales: object
 
     def __post_init__(self):
-        torch = _torch()
+        torch is None and _need_torch()
         k = self.k_codes
         if k.dim() != 4 or self.v_codes.shape != k.shape:
             raise ValueError("codes are [pages, heads, page_tokens, head_dim], K and V alike")
@@ -56,7 +63,7 @@ class KV8Cache:
 
 def kv8_cache(pages, heads, page_tokens=64, head_dim=128, device=None):
     """An empty cache: zero codes, smallest scales."""
-    torch = _torch()
+    torch is None and _need_torch()
     device = device or "cuda"
 
     def codes():
@@ -68,13 +75,12 @@ def kv8_cache(pages, heads, page_tokens=64, head_dim=128, device=None):
     return KV8Cache(codes(), codes(), scales(), scales())
 
 
-def _type(t):
-    torch = _torch()
-    if t.dtype is torch.bfloat16:
+def _type(kind):
+    if kind is torch.bfloat16:
         return NVFP4_BF16
-    if t.dtype is torch.float32:
+    if kind is torch.float32:
         return NVFP4_F32
-    raise TypeError("unsupported dtype %s" % t.dtype)
+    raise TypeError("unsupported dtype %s" % kind)
 
 
 def _call(name, index, stream, *args):
@@ -82,7 +88,6 @@ def _call(name, index, stream, *args):
     the last argument and with that device current."""
     if index < 0:
         raise ValueError("%s works on CUDA tensors" % name)
-    torch = _torch()
     fn = getattr(capi.load(), name)
     handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
     if torch._C._cuda_getDevice() == index:
@@ -95,16 +100,26 @@ def _call(name, index, stream, *args):
 
 
 def _packed(x, rows, cache, what):
-    """Strides of a [rows, heads, head_dim] tensor of the cache's device."""
-    if x.dim() != 3 or x.shape[0] != rows or x.shape[2] != cache.head_dim:
+    """Heads and strides of a [rows, heads, head_dim] tensor of the cache's device."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != cache.head_dim:
         raise ValueError("%s is [%d, heads, %d], not %s" % (what, rows, cache.head_dim,
-                                                            tuple(x.shape)))
+                                                            tuple(shape)))
     if x.get_device() != cache.index:
         raise ValueError("%s is not on the cache's device" % what)
     t, h, e = x.stride()
     if e != 1:
         raise ValueError("%s: the elements of a head are not contiguous" % what)
-    return t, h
+    return shape[1], t, h
+
+
+def _rows_of_cache(k, v, rows, cache):
+    """Strides of k and v, which have the cache's heads and one type."""
+    nk, kt, kh = _packed(k, rows, cache, "k")
+    nv, vt, vh = _packed(v, rows, cache, "v")
+    if nk != cache.heads or nv != nk or v.dtype is not k.dtype:
+        raise ValueError("k and v have the cache's heads and one type")
+    return kt, kh, vt, vh
 
 
 def _workspace(ws, cache):
@@ -114,18 +129,18 @@ def _workspace(ws, cache):
 
 
 def _batch(cache, page_table, lens, starts, rows, max_rows):
-    i32 = _torch().int32
+    i32 = torch.int32
     if not (page_table.dtype is i32 and lens.dtype is i32 and starts.dtype is i32):
         raise TypeError("page_table, lens and starts are int32 tensors")
     at = cache.index
     if page_table.get_device() != at or lens.get_device() != at or starts.get_device() != at:
         raise ValueError("page_table, lens and starts are on the cache's device")
-    n = lens.numel()
-    if page_table.dim() != 2 or lens.dim() != 1 or starts.dim() != 1 or (
-            page_table.shape[0] != n or starts.numel() != n + 1):
+    shape = page_table.shape
+    if len(shape) != 2 or lens.shape != shape[:1] or starts.dim() != 1 or (
+            starts.numel() != shape[0] + 1):
         raise ValueError("page_table is [n, pages], lens [n], starts [n + 1]")
+    n, width = shape
     stride, one = page_table.stride()
-    width = page_table.shape[1]
     if stride < width and n > 1:
         raise ValueError("page_table's rows overlap")
     if (one != 1 and width > 1) or not lens.is_contiguous() or not starts.is_contiguous():
@@ -139,7 +154,7 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     """One nvfp4_rope call: every tensor of xs ([tokens, heads, head_dim], of one
     type, strided) turned by positions (int32 [tokens, axes]).  With ``inverse``
     the gradients of xs from those of the outputs.  outs may be xs (in place)."""
-    torch = _torch()
+    torch is None and _need_torch()
     n, axes = len(xs), len(sections)
     if not 1 <= n <= 8 or not 1 <= axes <= 4:
         raise ValueError("rope takes 1 to 8 tensors and 1 to 4 sections")
@@ -148,16 +163,16 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
         outs = [torch.empty_like(x, memory_format=torch.contiguous_format) for x in xs]
     elif len(outs) != n:
         raise ValueError("rope has one output per tensor")
-    first = xs[0]
+    first, places = xs[0], positions.shape
     if first.dim() != 3:
         raise ValueError("rope's tensors are [tokens, heads, head_dim]")
     tokens, _, dim = first.shape
     at, kind = positions.get_device(), first.dtype
-    if positions.dtype is not torch.int32 or positions.dim() != 2 or (
-            positions.shape[0] != tokens or positions.shape[1] < axes):
+    if positions.dtype is not torch.int32 or len(places) != 2 or places[0] != tokens or (
+            places[1] < axes):
         raise ValueError("positions is int32 [tokens, axes]")
     stride, one = positions.stride()
-    if one != 1 and positions.shape[1] > 1:
+    if one != 1 and places[1] > 1:
         raise ValueError("positions' rows are contiguous")
     if tokens < 2:
         stride = axes
@@ -185,7 +200,7 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     pad = (0, 0, 0, 0)
     rp = _ROPE_PARAMS.pack(axes, *sections, *pad[axes:], theta, bool(interleaved), bool(per_axis),
                            bool(inverse))
-    _call("nvfp4_rope", at, stream, _ROPE_TENSORS[n].pack(*fields), n, _type(first), tokens, dim,
+    _call("nvfp4_rope", at, stream, _ROPE_TENSORS[n].pack(*fields), n, _type(kind), tokens, dim,
           positions.data_ptr(), stride, rp)
     return outs
 
@@ -194,14 +209,12 @@ def kv8_write(cache, k, v, page_table, lens, starts, max_new=None, ws=None, stre
     """One nvfp4_kv8_write call: rows starts[s]..starts[s+1] of k and v ([rows,
     heads, head_dim]) become sequence s's tokens from lens[s] on.  max_new: at
     least the most rows of a sequence (default: all rows)."""
+    torch is None and _need_torch()
     rows = k.shape[0]
-    kt, kh = _packed(k, rows, cache, "k")
-    vt, vh = _packed(v, rows, cache, "v")
-    if k.shape[1] != cache.heads or v.shape[1] != cache.heads or v.dtype is not k.dtype:
-        raise ValueError("k and v have the cache's heads and one type")
+    kt, kh, vt, vh = _rows_of_cache(k, v, rows, cache)
     b = _batch(cache, page_table, lens, starts, rows, rows if max_new is None else max_new)
     ws = workspace(0, cache.device) if ws is None else ws
-    _call("nvfp4_kv8_write", cache.index, stream, cache.desc, b, _type(k), k.data_ptr(), kt, kh,
+    _call("nvfp4_kv8_write", cache.index, stream, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
           v.data_ptr(), vt, vh, *_workspace(ws, cache))
 
 
@@ -209,22 +222,19 @@ def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype
              ws=None, stream=None):
     """One nvfp4_kv8_read call: sequence s's tokens from begins[s] on become rows
     starts[s]..starts[s+1] of the returned (k, v), [rows, heads, head_dim]."""
-    torch = _torch()
+    torch is None and _need_torch()
     if outs is None:
-        shape, kind = (rows, cache.heads, cache.head_dim), out_dtype or torch.bfloat16
-        outs = k, v = (torch.empty(shape, device=cache.device, dtype=kind),
-                       torch.empty(shape, device=cache.device, dtype=kind))
+        kind = out_dtype or torch.bfloat16
         kh = vh = cache.head_dim
         kt = vt = cache.heads * kh
+        k = torch.empty_strided((rows, cache.heads, kh), (kt, kh, 1), device=cache.device, dtype=kind)
+        outs = k, v = k, torch.empty_like(k)
     else:
         k, v = outs
-        kt, kh = _packed(k, rows, cache, "k")
-        vt, vh = _packed(v, rows, cache, "v")
-        if k.shape[1] != cache.heads or v.shape[1] != cache.heads or v.dtype is not k.dtype:
-            raise ValueError("k and v have the cache's heads and one type")
+        kt, kh, vt, vh = _rows_of_cache(k, v, rows, cache)
     b = _batch(cache, page_table, begins, starts, rows, rows if max_tokens is None else max_tokens)
     ws = workspace(0, cache.device) if ws is None else ws
-    _call("nvfp4_kv8_read", cache.index, stream, cache.desc, b, _type(k), k.data_ptr(), kt, kh,
+    _call("nvfp4_kv8_read", cache.index, stream, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
           v.data_ptr(), vt, vh, *_workspace(ws, cache))
     return outs
 
@@ -232,7 +242,7 @@ def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype
 def kv8_attention_workspace(cache, page_table, starts, q_heads, max_q):
     """Workspace for kv8_attention of these sizes, error word zeroed (the rest
     needs no initialization).  Serves one call in flight at a time."""
-    torch = _torch()
+    torch is None and _need_torch()
     ws = torch.empty(capi.nvfp4_kv8_attention_workspace_bytes(
         cache.heads, cache.head_dim, cache.page_tokens, q_heads, starts.numel() - 1, max_q,
         page_table.shape[1]), dtype=torch.uint8, device=cache.device)
@@ -246,19 +256,20 @@ def kv8_attention(q, cache, page_table, lens, starts, max_q=None, scale=None, ca
     s's queries in rows starts[s]..starts[s+1], over its lens[s] cached tokens.
     max_q: at least the most queries of a sequence (default: all rows).  lse: an
     fp32 [rows, q_heads] tensor that receives the log-sum-exps."""
-    torch = _torch()
+    torch is None and _need_torch()
     if q.dtype is not torch.bfloat16:
         raise TypeError("q and out are bfloat16")
     rows = q.shape[0]
-    qt, qh = _packed(q, rows, cache, "q")
-    q_heads = q.shape[1]
+    q_heads, qt, qh = _packed(q, rows, cache, "q")
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ot, oh = q_heads * cache.head_dim, cache.head_dim
     elif out.dtype is not torch.bfloat16:
         raise TypeError("q and out are bfloat16")
-    ot, oh = _packed(out, rows, cache, "out")
-    if out.shape[1] != q_heads:
-        raise ValueError("out has q's heads")
+    else:
+        heads, ot, oh = _packed(out, rows, cache, "out")
+        if heads != q_heads:
+            raise ValueError("out has q's heads")
     at = 0
     if lse is not None:
         if lse.dtype is not torch.float32 or lse.shape != (rows, q_heads) or (
