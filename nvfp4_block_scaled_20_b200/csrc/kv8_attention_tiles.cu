@@ -428,6 +428,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         // the L1 cache.)
         uint32_t s0_[32], s1_[32], s2_[32];
         auto hide = [&](uint32_t* s, int key) {
+          // most groups of a masked step are seen whole by the warp's rows (three
+          // prompts 404 us without this line, 394 with it)
+          if ((key >= all_lo || key + 32 <= a.sink) && key + 32 <= all_hi) return;
           const Seen see = seen_at(a, q.len, at);
           const uint32_t bits = (below(see.hi - key) & ~below(see.lo - key)) | below(see.sink - key);
 #pragma unroll
