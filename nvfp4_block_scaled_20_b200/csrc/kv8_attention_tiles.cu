@@ -34,7 +34,7 @@
 // work they stand for); one pass, two turns of 64 keys 1784; 96 and 32 keys
 // 1632 while the GPU is cool, 1700 to 1800 (1050 to 1110 TFLOP/s) in a loop that
 // holds it at its power limit.  What a tile costs besides its steps, 4736 rows
-// of 24 heads that see 128 keys: 57 with a thread on each row of q and out, 44
+// of 24 heads that see 128 keys: 57 with a thread on each row of q and out, 43
 // with a warp on each row.  Measured and not kept: two
 // softmax warps per row, an issuing thread per half (the halves fall into step
 // and wait together, 2300), the softmax warps issuing their own products
@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const __nv_bfloat16* src =
             static_cast<const __nv_bfloat16*>(a.q) + (q.first + i) * a.q_token +
             (int64_t)(unit.head * a.group + (mine ? row - i * a.group : 0)) * a.q_head;
-        constexpr int kAtOnce = 8;  // loads in flight; 16 spill: 419 us for 3 prompts, 405 so
+        constexpr int kAtOnce = 8;  // loads in flight; 16 spill: 416 us for 3 prompts, 394 so
 #pragma unroll 1
         for (int t0 = 0; t0 < kRowLanes; t0 += kAtOnce) {
           uint4 x[kAtOnce];
