@@ -542,8 +542,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         weights(s0_, 3);
         hand_over(&sm.p_full[h]);
       }
-      if (ok && n_steps > 0 &&
-          !warp_wait(smem_addr(&sm.o_full[h]), 0, gave_up, a.wait_limit_ns))
+      // The q tile becomes the stage of out, and at head size 128 a warp's part of
+      // it lies on q rows that other warps wrote: not before all have.  The last
+      // product comes after that; without steps the q tile itself is waited for.
+      if (ok && !warp_wait(smem_addr(n_steps > 0 ? &sm.o_full[h] : &sm.q_full), 0, gave_up,
+                           a.wait_limit_ns))
         ok = false;
       if (!ok) {
         *gave_up = 1;

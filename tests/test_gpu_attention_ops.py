@@ -626,3 +626,29 @@ def test_run_together_and_in_a_graph():
     for a, b in zip((c.k_codes, c.v_codes, c.k_scales, c.v_scales), kept):
         assert torch.equal(a, b)
     assert nv.device_error(ws[0]) == 0 and nv.device_error(ws_a) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq,n", [(200, 0), (130, 0), (600, 60)])
+def test_attention_rows_that_see_nothing_are_zero(nq, n, d):
+    """Tiles without a single step, of an empty sequence and, causal, before the
+    cache's first token: zeros and -infinity, whenever q arrives from memory."""
+    heads = 24
+    c = filled(4, heads, 64, d, 111)
+    t = i32([[2, 1]] * 4)
+    starts = i32([i * nq for i in range(5)])
+    q = torch.randn((4 * nq, heads, d), generator=gen(112), device=DEV).bfloat16()
+    out, lse = torch.empty_like(q), torch.empty((4 * nq, heads), device=DEV)
+    ws = nv.kv8_attention_workspace(c, t, starts, heads, nq)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    blind = torch.arange(4 * nq, device=DEV) % nq < nq - n  # at < 0
+    for k in range(40):
+        flush.fill_(k)
+        out.fill_(9.0)
+        lse.fill_(9.0)
+        nv.kv8_attention(q, c, t, i32([n] * 4), starts, max_q=nq, causal=True, out=out, lse=lse, ws=ws)
+        assert not out[blind].any()
+        assert (lse[blind] == -math.inf).all() and torch.isfinite(lse[~blind]).all()
+    for s in range(4 if n else 0):
+        rows = slice(s * nq, (s + 1) * nq)
+        check_sequence(out[rows], lse[rows], q[rows], c, t[s], n, causal=True)
