@@ -225,7 +225,9 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
   a.group = (int32_t)group;
   a.scale_log2 = (float)((double)qp->scale * 1.4426950408889634074);
   a.causal = qp->causal;
-  a.window = qp->window;
+  // places in a sequence are in -2^30 .. 2^30: a window of 2^30 hides nothing,
+  // and what the kernels subtract from a place stays in 32 bits
+  a.window = qp->window < (1 << 30) ? qp->window : (1 << 30);
   a.sink = qp->sink;
   const size_t need = nvfp4_kv8_attention_workspace_bytes(
       cache->heads, cache->head_dim, cache->page_tokens, qp->q_heads, batch->n, batch->max_rows,

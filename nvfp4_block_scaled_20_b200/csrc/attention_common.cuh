@@ -125,7 +125,8 @@ __device__ __forceinline__ bool load_query_seq(const Kv8Batch& b, int page_token
 }
 
 // Keys that a query sees: [lo, hi) and [0, sink).  `at`: the query's place in
-// its sequence of `len` cached tokens, negative before the cache's start.
+// its sequence of `len` cached tokens, negative before the cache's start, at least
+// -2^30, as a window is at most 2^30.
 struct Seen {
   int lo, hi, sink;
 };

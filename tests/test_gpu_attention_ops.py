@@ -652,3 +652,16 @@ def test_attention_rows_that_see_nothing_are_zero(nq, n, d):
     for s in range(4 if n else 0):
         rows = slice(s * nq, (s + 1) * nq)
         check_sequence(out[rows], lse[rows], q[rows], c, t[s], n, causal=True)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 30, 2 ** 31 - 5])
+@pytest.mark.parametrize("nq,n", [(3, 1), (5, 3), (700, 60), (90, 500)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_window_without_a_limit(window, nq, n, causal):
+    """The widest windows, with queries before the cache's first token: as if
+    there were none (causal, the last queries see what they see; else all)."""
+    for d, heads in ((128, 2), (64, 1)):
+        c, q, t, lens, starts, ws, out, lse = attend_case(
+            [nq, 1], [n, 40], heads, heads, d, 64, dict(causal=causal, window=window, sink=2), seed=121)
+        plain = nv.kv8_attention(q, c, t, lens, starts, max_q=nq, causal=causal, ws=ws)
+        assert torch.equal(out[:nq + 1], plain[:nq + 1])
