@@ -35,7 +35,8 @@ def _need_torch():
 class KV8Cache:
     """A paged KV cache in E4M3: codes uint8 [pages, heads, page_tokens,
     head_dim], one fp32 power-of-two scale per page and head [pages, heads].
-    Its tensors stay the ones that it was made of."""
+    Its tensors stay the ones that it was made of and keep their memory (no set_,
+    resize_ or .data on them).  A copy (copy.deepcopy, pickle) has its own."""
     k_codes: object
     v_codes: object
     k_scales: object
@@ -59,6 +60,11 @@ class KV8Cache:
             index=k.get_device(), desc=bytes(capi.nvfp4_kv8_cache(
                 k.data_ptr(), self.v_codes.data_ptr(), self.k_scales.data_ptr(),
                 self.v_scales.data_ptr(), *k.shape)))
+
+    def __reduce__(self):
+        # a copied or unpickled cache is made of its own tensors, and not given the
+        # addresses of this one's
+        return type(self), (self.k_codes, self.v_codes, self.k_scales, self.v_scales)
 
 
 def kv8_cache(pages, heads, page_tokens=64, head_dim=128, device=None):

@@ -220,3 +220,36 @@ def test_plain_attention_against_softmax():
         s = (q[:, h] @ k[:, h].T * 0.3).masked_fill(~ok, -math.inf)
         assert torch.allclose(out[:, h], torch.softmax(s, -1) @ v[:, h])
         assert torch.allclose(lse[:, h], torch.logsumexp(s, -1))
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "pickle", "save", "copy", "replace"])
+def test_a_copied_cache_names_its_own_memory(how):
+    import copy
+    import dataclasses
+    import io
+    import pickle
+    import nvfp4_block_scaled_20_b200 as nv
+    c = nv.kv8_cache(4, 2, 32, 64, device="cpu")
+    c.k_codes.random_(0, 120)
+    if how == "deepcopy":
+        d = copy.deepcopy([c])[0]
+    elif how == "pickle":
+        d = pickle.loads(pickle.dumps(c))
+    elif how == "save":
+        f = io.BytesIO()
+        torch.save(dict(cache=c), f)
+        f.seek(0)
+        d = torch.load(f, weights_only=False)["cache"]
+    elif how == "copy":
+        d = copy.copy(c)
+    else:
+        d = dataclasses.replace(c, k_codes=c.k_codes.clone())
+    names = ("k_codes", "v_codes", "k_scales", "v_scales")
+    at = capi.nvfp4_kv8_cache.from_buffer_copy(d.desc)
+    for n in names:
+        assert getattr(at, n) == getattr(d, n).data_ptr()
+        assert torch.equal(getattr(d, n), getattr(c, n))
+    own = [n for n in names if getattr(d, n).data_ptr() != getattr(c, n).data_ptr()]
+    assert own == {"copy": [], "replace": ["k_codes"]}.get(how, list(names))
+    assert (at.pages, at.heads, at.page_tokens, at.head_dim) == (4, 2, 32, 64)
+    assert (d.heads, d.page_tokens, d.head_dim, d.index) == (2, 32, 64, -1)
