@@ -3,7 +3,9 @@
 Torch-facing helpers of nvfp4_rope, nvfp4_kv8_write, nvfp4_kv8_read and
 nvfp4_kv8_attention (include/nvfp4.h): they check shapes and types, allocate
 outputs and marshal pointers and streams.  Work goes to the current stream of
-the tensors' device, or to ``stream``.
+the tensors' device, or to ``stream``.  What a call allocates itself belongs to
+the stream it works on; tensors that it is given are ordered by the caller, as
+for any other work on two streams.
 
 These calls are made once per layer and token, so the host side is kept short:
 the C structs are packed with ``struct`` (the formats below) instead of being
@@ -89,13 +91,24 @@ def _type(kind):
     raise TypeError("unsupported dtype %s" % kind)
 
 
-def _call(name, index, stream, *args):
-    """Calls the library with `stream`, or device `index`'s current stream, as
-    the last argument and with that device current."""
+def _on(stream, index, call, *args):
+    """call(*args) with `stream` current: the workspace and the outputs that it
+    allocates then belong to that stream -- their first use is ordered after
+    whatever had the memory before, and so is what gets it next."""
+    torch is None and _need_torch()
+    if stream.device.index != index:
+        raise ValueError("the stream is of another device than the tensors")
+    with torch.cuda.stream(stream):
+        return call(*args)
+
+
+def _call(name, index, *args):
+    """Calls the library with device `index`'s current stream as the last
+    argument and with that device current."""
     if index < 0:
         raise ValueError("%s works on CUDA tensors" % name)
     fn = getattr(capi.load(), name)
-    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    handle = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         st = fn(*args, handle)
     else:
@@ -160,6 +173,9 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     """One nvfp4_rope call: every tensor of xs ([tokens, heads, head_dim], of one
     type, strided) turned by positions (int32 [tokens, axes]).  With ``inverse``
     the gradients of xs from those of the outputs.  outs may be xs (in place)."""
+    if stream is not None:
+        return _on(stream, positions.get_device(), rope, xs, positions, sections, theta, interleaved,
+                   per_axis, inverse, outs)
     torch is None and _need_torch()
     n, axes = len(xs), len(sections)
     if not 1 <= n <= 8 or not 1 <= axes <= 4:
@@ -206,7 +222,7 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     pad = (0, 0, 0, 0)
     rp = _ROPE_PARAMS.pack(axes, *sections, *pad[axes:], theta, bool(interleaved), bool(per_axis),
                            bool(inverse))
-    _call("nvfp4_rope", at, stream, _ROPE_TENSORS[n].pack(*fields), n, _type(kind), tokens, dim,
+    _call("nvfp4_rope", at, _ROPE_TENSORS[n].pack(*fields), n, _type(kind), tokens, dim,
           positions.data_ptr(), stride, rp)
     return outs
 
@@ -215,12 +231,14 @@ def kv8_write(cache, k, v, page_table, lens, starts, max_new=None, ws=None, stre
     """One nvfp4_kv8_write call: rows starts[s]..starts[s+1] of k and v ([rows,
     heads, head_dim]) become sequence s's tokens from lens[s] on.  max_new: at
     least the most rows of a sequence (default: all rows)."""
+    if stream is not None:
+        return _on(stream, cache.index, kv8_write, cache, k, v, page_table, lens, starts, max_new, ws)
     torch is None and _need_torch()
     rows = k.shape[0]
     kt, kh, vt, vh = _rows_of_cache(k, v, rows, cache)
     b = _batch(cache, page_table, lens, starts, rows, rows if max_new is None else max_new)
     ws = workspace(0, cache.device) if ws is None else ws
-    _call("nvfp4_kv8_write", cache.index, stream, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
+    _call("nvfp4_kv8_write", cache.index, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
           v.data_ptr(), vt, vh, *_workspace(ws, cache))
 
 
@@ -228,6 +246,9 @@ def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype
              ws=None, stream=None):
     """One nvfp4_kv8_read call: sequence s's tokens from begins[s] on become rows
     starts[s]..starts[s+1] of the returned (k, v), [rows, heads, head_dim]."""
+    if stream is not None:
+        return _on(stream, cache.index, kv8_read, cache, page_table, begins, starts, rows, max_tokens,
+                   out_dtype, outs, ws)
     torch is None and _need_torch()
     if outs is None:
         kind = out_dtype or torch.bfloat16
@@ -240,7 +261,7 @@ def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype
         kt, kh, vt, vh = _rows_of_cache(k, v, rows, cache)
     b = _batch(cache, page_table, begins, starts, rows, rows if max_tokens is None else max_tokens)
     ws = workspace(0, cache.device) if ws is None else ws
-    _call("nvfp4_kv8_read", cache.index, stream, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
+    _call("nvfp4_kv8_read", cache.index, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
           v.data_ptr(), vt, vh, *_workspace(ws, cache))
     return outs
 
@@ -262,6 +283,9 @@ def kv8_attention(q, cache, page_table, lens, starts, max_q=None, scale=None, ca
     s's queries in rows starts[s]..starts[s+1], over its lens[s] cached tokens.
     max_q: at least the most queries of a sequence (default: all rows).  lse: an
     fp32 [rows, q_heads] tensor that receives the log-sum-exps."""
+    if stream is not None:
+        return _on(stream, cache.index, kv8_attention, q, cache, page_table, lens, starts, max_q,
+                   scale, causal, window, sink, out, lse, ws)
     torch is None and _need_torch()
     if q.dtype is not torch.bfloat16:
         raise TypeError("q and out are bfloat16")
@@ -291,5 +315,5 @@ def kv8_attention(q, cache, page_table, lens, starts, max_q=None, scale=None, ca
         scale = 1.0 / math.sqrt(cache.head_dim)
     query = _QUERY.pack(q.data_ptr(), out.data_ptr(), at, q_heads, qt, qh, ot, oh, scale,
                         bool(causal), window, sink)
-    _call("nvfp4_kv8_attention", cache.index, stream, cache.desc, b, query, *_workspace(ws, cache))
+    _call("nvfp4_kv8_attention", cache.index, cache.desc, b, query, *_workspace(ws, cache))
     return out

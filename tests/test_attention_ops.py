@@ -253,3 +253,20 @@ def test_a_copied_cache_names_its_own_memory(how):
     assert own == {"copy": [], "replace": ["k_codes"]}.get(how, list(names))
     assert (at.pages, at.heads, at.page_tokens, at.head_dim) == (4, 2, 32, 64)
     assert (d.heads, d.page_tokens, d.head_dim, d.index) == (2, 32, 64, -1)
+
+
+def test_a_stream_of_another_device_is_refused():
+    import nvfp4_block_scaled_20_b200 as nv
+
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 3), 0
+
+    c = nv.kv8_cache(4, 2, 32, 64, device="cpu")
+    k, one = torch.zeros(3, 2, 64), torch.zeros(1, dtype=torch.int32)
+    t, starts = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: nv.kv8_write(c, k, k, t, one, starts, ws=one, stream=Stream()),
+                 lambda: nv.kv8_read(c, t, one, starts, 3, stream=Stream()),
+                 lambda: nv.kv8_attention(k.bfloat16(), c, t, one, starts, ws=one, stream=Stream()),
+                 lambda: nv.rope([k], torch.zeros((3, 1), dtype=torch.int32), [4], stream=Stream())):
+        with pytest.raises(ValueError, match="another device"):
+            call()

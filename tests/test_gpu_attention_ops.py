@@ -665,3 +665,55 @@ def test_attention_window_without_a_limit(window, nq, n, causal):
             [nq, 1], [n, 40], heads, heads, d, 64, dict(causal=causal, window=window, sink=2), seed=121)
         plain = nv.kv8_attention(q, c, t, lens, starts, max_q=nq, causal=causal, ws=ws)
         assert torch.equal(out[:nq + 1], plain[:nq + 1])
+
+
+@pytest.mark.parametrize("call", ["token", "chunk", "read", "rope", "write"])
+def test_what_a_call_allocates_belongs_to_its_stream(call):
+    """A call on a stream of its own, without workspace and outputs, while either
+    stream is behind the other: memory that the call takes or gives back is not
+    used by the other stream's work meanwhile."""
+    heads, d, n = 2, 128, 4000
+    c = filled(64, heads, 64, d, 131)
+    t = torch.arange(63, device=DEV, dtype=torch.int32)[None].contiguous()
+    nq = dict(token=1, chunk=700).get(call, 500)
+    x = torch.randn((nq, heads, d), generator=gen(132), device=DEV).bfloat16()
+    lens, starts, zero, minus = i32([n]), i32([0, nq]), i32([0]), -x
+    pos = torch.arange(nq, device=DEV, dtype=torch.int32)[:, None].contiguous()
+
+    def go(stream=None):
+        if call == "read":
+            return nv.kv8_read(c, t, zero, starts, nq, stream=stream)[0]
+        if call == "rope":
+            return nv.rope([x], pos, [64], stream=stream)[0]
+        if call == "write":
+            nv.kv8_write(c, x, minus, t, zero, starts, stream=stream)
+            return c.v_codes
+        return nv.kv8_attention(x, c, t, lens, starts, stream=stream)
+
+    want = go().clone()
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    size = max(want.numel() * want.element_size(),
+               nv.kv8_attention_workspace(c, t, starts, heads, nq).numel())
+    torch.cuda.synchronize()
+    for _ in range(3):
+        # the call's kernels come late: what this stream allocates now is not theirs
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(30_000_000)
+        got = go(side)
+        mine = [torch.full((s,), 7, dtype=torch.uint8, device=DEV) for s in (size, size, 256, 512)]
+        here.synchronize()
+        side.synchronize()
+        assert torch.equal(got, want)
+        assert all((m == 7).all() for m in mine)
+        # they come early: what this stream has yet to read is not overwritten
+        mine = [torch.full((s,), 3, dtype=torch.uint8, device=DEV) for s in (size, size, 256, 512)]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(30_000_000)
+        sums = [m.clone() for m in mine]
+        del mine
+        got = go(side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            assert torch.equal(got, want)
+        here.synchronize()
+        assert all((m == 3).all() for m in sums)
