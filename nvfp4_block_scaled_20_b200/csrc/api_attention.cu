@@ -73,6 +73,7 @@ nvfp4_status write_or_read(bool write, const nvfp4_kv8_cache* cache, const nvfp4
     if (!aligned(strides[i] * elem_bytes(dtype), 16)) return NVFP4_ERR_ALIGN;
   }
   if (!ws || ws_bytes < nvfp4_workspace_bytes(0)) return NVFP4_ERR_WORKSPACE;
+  if (!aligned(ws, 4)) return NVFP4_ERR_ALIGN;  // the error word
   // one CTA per page that a sequence may touch, head, K and V: a grid dimension
   if (((int64_t)batch->max_rows / cache->page_tokens + 2) * cache->heads * 2 > INT32_MAX)
     return NVFP4_ERR_SHAPE;

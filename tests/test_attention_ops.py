@@ -270,3 +270,12 @@ def test_a_stream_of_another_device_is_refused():
                  lambda: nv.rope([k], torch.zeros((3, 1), dtype=torch.int32), [4], stream=Stream())):
         with pytest.raises(ValueError, match="another device"):
             call()
+
+
+@pytest.mark.parametrize("call", ["write", "read"])
+def test_cache_calls_refuse_a_misaligned_workspace(call):
+    """The error word is written by an atomic of four bytes."""
+    fn = capi.nvfp4_kv8_write if call == "write" else capi.nvfp4_kv8_read
+    for shift in (1, 2, 3):
+        assert fn(_cache(), _batch(), 1, A, 1024, 128, A, 1024, 128, A + shift,
+                  capi.nvfp4_workspace_bytes(0), None) == ALIGN
