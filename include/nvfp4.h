@@ -427,6 +427,8 @@ typedef struct nvfp4_rope_params {
  * Angles are products in double, so far positions keep theirs.
  *   positions  device int32 [tokens, positions_stride], one per axis (any
  *              value, negative ones too).
+ * Outputs do not overlap each other or another tensor's x, and the rows of an
+ * output lie apart (what shows in the pointers and strides is refused).
  * Shape: head_dim even, 2..512; sum(sections) <= head_dim / 2.  Alignment: two
  * elements for pointers, even strides (wider when the strides allow: 16-byte
  * loads).  Takes no workspace. */
@@ -502,7 +504,8 @@ NVFP4_API nvfp4_status nvfp4_kv8_write(const nvfp4_kv8_cache* cache, const nvfp4
 
 /* Reads tokens back: sequence s's tokens lens[s], lens[s] + 1, ... become its
  * packed rows of k and v, code * scale rounded to dtype.  Arguments as
- * nvfp4_kv8_write (k and v are outputs; the cache is only read). */
+ * nvfp4_kv8_write (k and v are outputs, which do not overlap and whose rows lie
+ * apart; the cache is only read). */
 NVFP4_API nvfp4_status nvfp4_kv8_read(const nvfp4_kv8_cache* cache, const nvfp4_kv8_batch* batch,
                                       int32_t dtype, void* k, int64_t k_token_stride,
                                       int64_t k_head_stride, void* v, int64_t v_token_stride,
@@ -511,8 +514,8 @@ NVFP4_API nvfp4_status nvfp4_kv8_read(const nvfp4_kv8_cache* cache, const nvfp4_
 
 /* Queries of an attention call.
  *   q, out   device bf16 [rows, q_heads, head_dim], strides in elements
- *            (multiples of 8), 16-byte aligned; q_heads a multiple of the
- *            cache's heads (query head h reads KV head h / (q_heads / heads)).
+ *            (multiples of 8; the rows of out lie apart), 16-byte aligned;
+ *            q_heads a multiple of the cache's heads (query head h reads KV head h / (q_heads / heads)).
  *   lse      device fp32 [rows, q_heads] or NULL: log of the sum of the
  *            exponentials (natural), -infinity for a row that sees nothing.
  *   scale    of the scores, > 0 (1 / sqrt(head_dim) as a rule).

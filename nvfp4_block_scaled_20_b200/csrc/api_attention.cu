@@ -19,6 +19,16 @@ inline bool dtype_ok(int32_t dt) { return dt == NVFP4_F32 || dt == NVFP4_BF16; }
 inline cudaStream_t S(void* s) { return static_cast<cudaStream_t>(s); }
 nvfp4_status cuda_status(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA; }
 
+// Whether the rows of `dim` elements that a call writes at i s0 + j s1, i < n0 and
+// j < n1, lie apart: one stride steps over a row, the other over all rows of the
+// first.  (An expanded output would get what CTAs store in any order.)
+bool rows_apart(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t dim) {
+  if (n0 <= 1) return n1 <= 1 || s1 >= dim;
+  if (n1 <= 1) return s0 >= dim;
+  if (s0 < s1) return rows_apart(n1, s1, n0, s0, dim);
+  return s1 >= dim && (s0 - dim) / s1 >= n1 - 1;
+}
+
 // Partial results follow the error word in the workspace.
 constexpr size_t kPartOffset = 256;
 
@@ -72,8 +82,12 @@ nvfp4_status write_or_read(bool write, const nvfp4_kv8_cache* cache, const nvfp4
     if (strides[i] < 0) return NVFP4_ERR_SHAPE;
     if (!aligned(strides[i] * elem_bytes(dtype), 16)) return NVFP4_ERR_ALIGN;
   }
+  for (int i = 0; i < 4 && !write; i += 2)
+    if (!rows_apart(batch->rows, strides[i], cache->heads, strides[i + 1], cache->head_dim))
+      return NVFP4_ERR_SHAPE;
   if (!ws || ws_bytes < nvfp4_workspace_bytes(0)) return NVFP4_ERR_WORKSPACE;
   if (!aligned(ws, 4)) return NVFP4_ERR_ALIGN;  // the error word
+  if (!write && k == v) return NVFP4_ERR_INVALID_ARG;
   // one CTA per page that a sequence may touch, head, K and V: a grid dimension
   if (((int64_t)batch->max_rows / cache->page_tokens + 2) * cache->heads * 2 > INT32_MAX)
     return NVFP4_ERR_SHAPE;
@@ -123,10 +137,22 @@ nvfp4_status nvfp4_rope(const nvfp4_rope_tensor* tensors, int32_t n, int32_t dty
       if (s % 2) return NVFP4_ERR_ALIGN;  // pairs of elements
     }
     if (!aligned(t.x, 2 * eb) || !aligned(t.out, 2 * eb)) return NVFP4_ERR_ALIGN;
+    if (!rows_apart(tokens, t.out_token_stride, t.heads, t.out_head_stride, head_dim))
+      return NVFP4_ERR_SHAPE;
     a.t[a.n++] = RopeTensor{t.x, t.out, t.x_token_stride, t.x_head_stride, t.out_token_stride,
                             t.out_head_stride, (int32_t)t.heads, 0, 0, 0};
   }
   if (tokens == 0 || a.n == 0) return NVFP4_OK;
+  // an output may take the place of its own input, element by element, and of
+  // nothing else that the call reads or writes
+  for (int i = 0; i < a.n; ++i) {
+    const RopeTensor& t = a.t[i];
+    if (t.out == t.x && ((tokens > 1 && t.out_token != t.x_token) ||
+                         (t.heads > 1 && t.out_head != t.x_head)))
+      return NVFP4_ERR_INVALID_ARG;
+    for (int j = 0; j < a.n; ++j)
+      if (j != i && (t.out == a.t[j].out || t.out == a.t[j].x)) return NVFP4_ERR_INVALID_ARG;
+  }
   if (!positions) return NVFP4_ERR_INVALID_ARG;
   if (!aligned(positions, 4)) return NVFP4_ERR_ALIGN;
   // turns per position: theta^-(j / pairs of the axis) or theta^-(i / all pairs),
@@ -211,6 +237,9 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
   }
   if (!aligned(qp->q, 16) || !aligned(qp->out, 16) || (qp->lse && !aligned(qp->lse, 4)))
     return NVFP4_ERR_ALIGN;
+  if (!rows_apart(batch->rows, qp->out_token_stride, qp->q_heads, qp->out_head_stride,
+                  cache->head_dim))
+    return NVFP4_ERR_SHAPE;
   Kv8Attention a;
   std::memset(&a, 0, sizeof(a));
   a.c = cache_of(cache);

@@ -279,3 +279,60 @@ def test_cache_calls_refuse_a_misaligned_workspace(call):
     for shift in (1, 2, 3):
         assert fn(_cache(), _batch(), 1, A, 1024, 128, A, 1024, 128, A + shift,
                   capi.nvfp4_workspace_bytes(0), None) == ALIGN
+
+
+OVERLAPS = [(0, 128), (1024, 0), (1024, 120), (1000, 128), (896, 128), (128, 128), (136, 128)]
+APART = [(1024, 128), (2048, 128), (128, 6 * 128), (256, 16 * 128), (1032, 128)]
+
+
+def test_outputs_whose_rows_overlap_are_refused():
+    """[6 rows, 8 heads, 128]: token and head strides.  The next check refuses the
+    calls whose rows lie apart: no call here reaches a launch."""
+    ws = capi.nvfp4_workspace_bytes(0)
+
+    def read(strides):
+        return capi.nvfp4_kv8_read(_cache(), _batch(), 1, A, *strides[:2], 2 * A, *strides[2:], None,
+                                   ws, None)
+
+    def attend(strides):
+        d = dict(q=A, out=2 * A, lse=None, q_heads=8, q_token_stride=0, q_head_stride=0,
+                 out_token_stride=strides[0], out_head_stride=strides[1], scale=0.1, causal=1,
+                 window=-1, sink=0)
+        return capi.nvfp4_kv8_attention(_cache(), _batch(), capi.nvfp4_kv8_query(**d), None, ws, None)
+
+    def rope(strides, **kw):
+        return _rope(out=2 * A, heads=8, tokens=6, strides=(0, 0, *strides), pos=None, **kw)
+
+    good = (1024, 128)
+    for bad in OVERLAPS:
+        assert read(good + bad) == SHAPE and read(bad + good) == SHAPE, bad
+        assert attend(bad) == SHAPE and rope(bad) == SHAPE, bad
+    for ok in APART:  # no workspace, no positions
+        assert read(ok + good) == WORKSPACE and read(good + ok) == WORKSPACE, ok
+        assert attend(ok) == WORKSPACE and rope(ok) == INVALID, ok
+    # one tensor for both (the size of the launch would be refused next)
+    many = dict(cache=_cache(heads=32767), batch=_batch(max_rows=1 << 30))
+    wide = (32767 * 128, 128)
+    for v, want in ((A, INVALID), (2 * A, SHAPE)):
+        assert capi.nvfp4_kv8_read(many["cache"], many["batch"], 1, A, *wide, v, *wide, A, ws,
+                                   None) == want
+    # one token, one head: a stride that is not used may be anything
+    assert _rope(out=2 * A, heads=8, tokens=1, strides=(0, 0, 0, 128), pos=None) == INVALID
+    assert _rope(out=2 * A, heads=1, tokens=6, strides=(0, 0, 128, 0), pos=None) == INVALID
+
+
+def test_rope_refuses_outputs_in_the_place_of_other_tensors():
+    def go(*tensors):  # (x, out, token stride of x)
+        t = (capi.nvfp4_rope_tensor * len(tensors))()
+        for i, (x, out, xt) in enumerate(tensors):
+            t[i] = capi.nvfp4_rope_tensor(x, out, 8, xt, 128, 1024, 128)
+        rp = capi.nvfp4_rope_params(3, (22, 21, 21), 1e4, 1, 1, 0)
+        # (a position that is not aligned ends the calls that pass)
+        return capi.nvfp4_rope(t, len(tensors), 1, 6, 128, A + 2, 3, rp, None)
+
+    assert go((A, A, 1024), (2 * A, 2 * A, 1024)) == ALIGN  # in place
+    assert go((A, 2 * A, 1024), (A, 3 * A, 1024)) == ALIGN  # one input twice
+    assert go((A, 2 * A, 1024), (2 * A, A, 1024)) == INVALID  # swapped
+    assert go((A, 3 * A, 1024), (2 * A, 3 * A, 1024)) == INVALID
+    assert go((A, A, 1024), (A, 2 * A, 1024)) == INVALID
+    assert go((A, A, 2048)) == INVALID
