@@ -605,11 +605,13 @@ NVFP4_API nvfp4_status nvfp4_convert_sweep(int32_t target, uint32_t first_bits, 
 NVFP4_API nvfp4_status nvfp4_set_wait_limit(uint64_t ns);
 
 /* Test hook of the timeout path, for the whole process, read at each
- * nvfp4_gemm call: with on = 1 every GEMM's MMA issuer first waits on a
- * barrier that nothing ever completes, while the producers' first stages are
- * in flight; the wait runs out after the nvfp4_set_wait_limit bound and the
- * kernel takes its abort path (NVFP4_ERR_TIMEOUT in the error word, output
- * not written).  on = 0 (the default) turns it off; other values return
+ * nvfp4_gemm and nvfp4_kv8_attention call: with on = 1 every GEMM's MMA issuer
+ * first waits on a barrier that nothing ever completes, while the producers'
+ * first stages are in flight, and every CTA of an attention leaves out its first
+ * copy of codes, which others wait for while the following ones are in flight.
+ * The wait runs out after the nvfp4_set_wait_limit bound and the kernel takes its
+ * abort path (NVFP4_ERR_TIMEOUT in the error word; a GEMM's output is not
+ * written, an attention's is not to be used).  on = 0 (the default) turns it off; other values return
  * NVFP4_ERR_INVALID_ARG. */
 NVFP4_API nvfp4_status nvfp4_set_test_stall(int32_t on);
 

@@ -267,6 +267,7 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
   a.err = static_cast<uint32_t*>(ws);
   a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPartOffset);
   a.wait_limit_ns = gemm_wait_limit_ns();
+  a.stall = gemm_test_stall();
   return cuda_status(launch_kv8_attention(a, S(stream)));
 }
 

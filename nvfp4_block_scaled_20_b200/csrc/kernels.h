@@ -103,7 +103,8 @@ struct GemmArgs {
 // them (0: it runs unsplit).
 int64_t gemm_split_slabs(int64_t M, int64_t N, int64_t K, int32_t epilogue);
 
-// Default bound of a GEMM pipeline wait, and the process-wide settings
+// Default bound of a pipeline wait of the GEMM and of attention, and the
+// process-wide settings
 // (nvfp4_set_wait_limit, 0 restores the default; nvfp4_set_test_stall).
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;
 uint64_t gemm_wait_limit_ns();

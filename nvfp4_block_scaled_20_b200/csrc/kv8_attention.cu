@@ -268,15 +268,16 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(kDim, kTiles))
         const bool mine_now = lane >= from && lane < from + pieces;
         const uint32_t here = __ballot_sync(0xFFFFFFFFu, mine_now && page >= 0);
         const uint32_t full = smem_addr(&sm.full[st]);
+        const bool stalled = a.stall && issued == 0;  // test hook: never announced nor copied
         if (mine_now) {
           const int p = lane - from;
           const float2 sc = make_float2(ks, vs);
           for (int k = 0; k < per_piece; ++k) sm.scale[st][p * per_piece + k] = sc;
         }
         __syncwarp();
-        if (lane == 0) bar_expect(full, __popc(here) * 2 * piece_bytes);
+        if (lane == 0 && !stalled) bar_expect(full, __popc(here) * 2 * piece_bytes);
         __syncwarp();
-        if (mine_now && page >= 0) {
+        if (mine_now && page >= 0 && !stalled) {
           const int p = lane - from;
           const int key = step_at(steps, i) * kStepKeys + p * piece_keys;
           const int64_t off = ((page * a.c.heads + head) * pt + key % pt) * kDim;
