@@ -542,9 +542,12 @@ typedef struct nvfp4_kv8_query {
  * The codes enter the matrix products as they are (fp16, exact), the scales in
  * fp32 beside them; scores, maxima and sums in fp32; the softmax weights are
  * rounded to fp16 for the product with V.  A query that sees nothing gets
- * zeros.  Codes that no query of a tile sees are never used, whatever they are;
- * a NaN among a token's values may reach queries of the same call that do not
- * see that token when others of the same 128-row tile do.
+ * zeros.  A NaN among a token's keys makes the queries that see the token NaN and
+ * reaches no others.  A NaN among its values makes that element NaN in the queries
+ * that see the token, and possibly (0 * NaN) in queries that do not, but share a
+ * tile with one that does: 256 rows of one sequence and KV head, a row being a
+ * query and query head, in that order.  Tokens that no query of a tile sees are
+ * not used, whatever they hold.
  * Workspace: nvfp4_kv8_attention_workspace_bytes, 16-byte aligned (the error
  * word, zero at first, and partial results of key ranges, joined in the order
  * of the keys: the result is deterministic).  One call in flight per

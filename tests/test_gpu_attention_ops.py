@@ -717,3 +717,42 @@ def test_what_a_call_allocates_belongs_to_its_stream(call):
             assert torch.equal(got, want)
         here.synchronize()
         assert all((m == 3).all() for m in sums)
+
+
+@pytest.mark.parametrize("nq,n,hq,hk,d,pt", [
+    (1, 300, 4, 4, 128, 64), (5, 40, 6, 2, 64, 32), (7, 900, 8, 4, 128, 128), (4, 20000, 8, 2, 64, 64),
+    (200, 700, 2, 1, 128, 64), (300, 300, 3, 3, 64, 32), (600, 2100, 4, 2, 128, 128),
+    (40, 9000, 12, 2, 64, 64)])
+@pytest.mark.parametrize("mask", [0, 1, 2, 3])
+def test_attention_nan_values_stay_in_their_element_and_tile(nq, n, hq, hk, d, pt, mask):
+    """A NaN among a token's values makes that element of the queries that see the
+    token NaN.  Of the others only rows of a tile of 256 that holds a query which
+    sees it may be NaN there; nothing else changes, other heads, elements and
+    sequences included."""
+    kw = MASKS[mask]
+    pages = -(-n // pt) + 1
+    c = filled(pages + 2, hk, pt, d, 151)
+    order = torch.randperm(pages + 2, generator=gen(152), device=DEV).to(torch.int32)
+    t = torch.stack([order[:pages], order[-2:].repeat(pages)[:pages]]).contiguous()
+    q = torch.randn((nq + 2, hq, d), generator=gen(153), device=DEV).bfloat16()
+    args = (t, i32([n, 30]), i32([0, nq, nq + 2]))
+    lse = [torch.empty((nq + 2, hq), device=DEV) for _ in "ab"]
+    clean = nv.kv8_attention(q, c, *args, max_q=nq + 1, lse=lse[0], **kw)
+    must = torch.zeros((nq + 2, hq, d), dtype=torch.bool, device=DEV)
+    may = torch.zeros_like(must)
+    ok = ref.seen(nq, n, kw["causal"], kw.get("window", -1), kw.get("sink", 0), DEV)
+    g = hq // hk
+    tile = (torch.arange(nq, device=DEV)[:, None] * g + torch.arange(g, device=DEV)) // 256  # [nq, g]
+    for i, (key, col) in enumerate([(0, 3), (3, 40), (n // 2, 17), (n - nq, 0), (n - nq // 2 - 1, d - 1),
+                                    (n - 1, 33), (n - 1, 31), (max(0, n - 120), 5), (n - nq // 3 - 1, 62)]):
+        head = i % hk
+        c.v_codes[t[0, key // pt].long(), head, key % pt, col] = (0x7F, 0xFF)[i % 2]
+        group = slice(head * g, (head + 1) * g)
+        sees = ok[:, key]
+        must[:nq, group, col] |= sees[:, None]
+        may[:nq, group, col] |= torch.isin(tile, tile[sees])
+    out = nv.kv8_attention(q, c, *args, max_q=nq + 1, lse=lse[1], **kw)
+    assert out[must].isnan().all()
+    assert torch.equal(out[~may], clean[~may])
+    assert (out[may].isnan() | (out[may] == clean[may])).all()
+    assert torch.equal(lse[0], lse[1])
