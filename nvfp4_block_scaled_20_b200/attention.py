@@ -102,12 +102,11 @@ def _on(stream, index, call, *args):
         return call(*args)
 
 
-def _call(name, index, *args):
-    """Calls the library with device `index`'s current stream as the last
+def _call(fn, index, *args):
+    """fn, a call of capi, with device `index`'s current stream as the last
     argument and with that device current."""
     if index < 0:
-        raise ValueError("%s works on CUDA tensors" % name)
-    fn = getattr(capi.load(), name)
+        raise ValueError("%s works on CUDA tensors" % fn.__name__)
     handle = torch._C._cuda_getCurrentRawStream(index)
     if torch._C._cuda_getDevice() == index:
         st = fn(*args, handle)
@@ -115,7 +114,7 @@ def _call(name, index, *args):
         with torch.cuda.device(index):
             st = fn(*args, handle)
     if st:
-        raise capi.NVFP4Error(name, st)
+        raise capi.NVFP4Error(fn.__name__, st)
 
 
 def _packed(x, rows, cache, what):
@@ -222,7 +221,7 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     pad = (0, 0, 0, 0)
     rp = _ROPE_PARAMS.pack(axes, *sections, *pad[axes:], theta, bool(interleaved), bool(per_axis),
                            bool(inverse))
-    _call("nvfp4_rope", at, _ROPE_TENSORS[n].pack(*fields), n, _type(kind), tokens, dim,
+    _call(capi.nvfp4_rope, at, _ROPE_TENSORS[n].pack(*fields), n, _type(kind), tokens, dim,
           positions.data_ptr(), stride, rp)
     return outs
 
@@ -238,7 +237,7 @@ def kv8_write(cache, k, v, page_table, lens, starts, max_new=None, ws=None, stre
     kt, kh, vt, vh = _rows_of_cache(k, v, rows, cache)
     b = _batch(cache, page_table, lens, starts, rows, rows if max_new is None else max_new)
     ws = workspace(0, cache.device) if ws is None else ws
-    _call("nvfp4_kv8_write", cache.index, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
+    _call(capi.nvfp4_kv8_write, cache.index, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
           v.data_ptr(), vt, vh, *_workspace(ws, cache))
 
 
@@ -261,7 +260,7 @@ def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype
         kt, kh, vt, vh = _rows_of_cache(k, v, rows, cache)
     b = _batch(cache, page_table, begins, starts, rows, rows if max_tokens is None else max_tokens)
     ws = workspace(0, cache.device) if ws is None else ws
-    _call("nvfp4_kv8_read", cache.index, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
+    _call(capi.nvfp4_kv8_read, cache.index, cache.desc, b, _type(k.dtype), k.data_ptr(), kt, kh,
           v.data_ptr(), vt, vh, *_workspace(ws, cache))
     return outs
 
@@ -315,5 +314,5 @@ def kv8_attention(q, cache, page_table, lens, starts, max_q=None, scale=None, ca
         scale = 1.0 / math.sqrt(cache.head_dim)
     query = _QUERY.pack(q.data_ptr(), out.data_ptr(), at, q_heads, qt, qh, ot, oh, scale,
                         bool(causal), window, sink)
-    _call("nvfp4_kv8_attention", cache.index, cache.desc, b, query, *_workspace(ws, cache))
+    _call(capi.nvfp4_kv8_attention, cache.index, cache.desc, b, query, *_workspace(ws, cache))
     return out

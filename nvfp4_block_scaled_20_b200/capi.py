@@ -45,33 +45,38 @@ class nvfp4_tensor_desc(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64)]
 
 
-class nvfp4_rope_tensor(ctypes.Structure):
+class _ByAddress(ctypes.Structure):
+    """A struct that a call with a pointer argument takes by its address."""
+    _as_parameter_ = property(ctypes.byref)
+
+
+class nvfp4_rope_tensor(_ByAddress):
     _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64),
                 ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
                 ("out_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64)]
 
 
-class nvfp4_rope_params(ctypes.Structure):
+class nvfp4_rope_params(_ByAddress):
     _fields_ = [("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4),
                 ("theta", ctypes.c_double), ("interleaved", ctypes.c_int32),
                 ("per_axis", ctypes.c_int32), ("inverse", ctypes.c_int32)]
 
 
-class nvfp4_kv8_cache(ctypes.Structure):
+class nvfp4_kv8_cache(_ByAddress):
     _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
                 ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
                 ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
                 ("page_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
-class nvfp4_kv8_batch(ctypes.Structure):
+class nvfp4_kv8_batch(_ByAddress):
     _fields_ = [("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
                 ("table_pages", ctypes.c_int32), ("lens", ctypes.c_void_p),
                 ("starts", ctypes.c_void_p), ("n", ctypes.c_int32), ("rows", ctypes.c_int64),
                 ("max_rows", ctypes.c_int32)]
 
 
-class nvfp4_kv8_query(ctypes.Structure):
+class nvfp4_kv8_query(_ByAddress):
     _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
                 ("q_heads", ctypes.c_int32), ("q_token_stride", ctypes.c_int64),
                 ("q_head_stride", ctypes.c_int64), ("out_token_stride", ctypes.c_int64),
@@ -252,31 +257,27 @@ def nvfp4_set_test_stall(on):
     return _call("nvfp4_set_test_stall", on)
 
 
-def _at(x):
-    """Address of a struct given as a ctypes Structure or as its packed bytes."""
-    return x if isinstance(x, bytes) else ctypes.byref(x)
-
-
+# Called once per layer and token, so straight to the library; structs are given as
+# ctypes Structures or as their packed bytes.
 def nvfp4_rope(tensors, n, dtype, tokens, head_dim, positions, positions_stride, rp, stream):
-    return _call("nvfp4_rope", tensors, n, dtype, tokens, head_dim, positions, positions_stride,
-                 _at(rp), stream)
+    return load().nvfp4_rope(tensors, n, dtype, tokens, head_dim, positions, positions_stride,
+                             rp, stream)
 
 
 def nvfp4_kv8_write(cache, batch, dtype, k, k_token, k_head, v, v_token, v_head, ws, ws_bytes,
                     stream):
-    return _call("nvfp4_kv8_write", _at(cache), _at(batch), dtype, k, k_token,
-                 k_head, v, v_token, v_head, ws, ws_bytes, stream)
+    return load().nvfp4_kv8_write(cache, batch, dtype, k, k_token, k_head, v, v_token,
+                                  v_head, ws, ws_bytes, stream)
 
 
 def nvfp4_kv8_read(cache, batch, dtype, k, k_token, k_head, v, v_token, v_head, ws, ws_bytes,
                    stream):
-    return _call("nvfp4_kv8_read", _at(cache), _at(batch), dtype, k, k_token,
-                 k_head, v, v_token, v_head, ws, ws_bytes, stream)
+    return load().nvfp4_kv8_read(cache, batch, dtype, k, k_token, k_head, v, v_token,
+                                 v_head, ws, ws_bytes, stream)
 
 
 def nvfp4_kv8_attention(cache, batch, query, ws, ws_bytes, stream):
-    return _call("nvfp4_kv8_attention", _at(cache), _at(batch),
-                 _at(query), ws, ws_bytes, stream)
+    return load().nvfp4_kv8_attention(cache, batch, query, ws, ws_bytes, stream)
 
 
 def nvfp4_kv8_attention_workspace_bytes(heads, head_dim, page_tokens, q_heads, n, max_rows,
