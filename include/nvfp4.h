@@ -610,8 +610,8 @@ NVFP4_API nvfp4_status nvfp4_set_wait_limit(uint64_t ns);
 /* Test hook of the timeout path, for the whole process, read at each
  * nvfp4_gemm and nvfp4_kv8_attention call: with on = 1 every GEMM's MMA issuer
  * first waits on a barrier that nothing ever completes, while the producers'
- * first stages are in flight, and every CTA of an attention leaves out its first
- * copy of codes, which others wait for while the following ones are in flight.
+ * first stages are in flight, and in every CTA of an attention the first copy of
+ * codes is waited for in vain while it and the following ones arrive.
  * The wait runs out after the nvfp4_set_wait_limit bound and the kernel takes its
  * abort path (NVFP4_ERR_TIMEOUT in the error word; a GEMM's output is not
  * written, an attention's is not to be used).  on = 0 (the default) turns it off; other values return

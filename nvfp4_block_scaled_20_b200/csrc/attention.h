@@ -77,7 +77,9 @@ struct Kv8Attention {
   uint32_t* err;
   float* part;  // partial results of split tiles (workspace)
   uint64_t wait_limit_ns;
-  int32_t stall;  // test hook (nvfp4_set_test_stall): a CTA's first copy is left out
+  // test hook (nvfp4_set_test_stall), 0 or 1: an arrival that the first copies'
+  // barrier of a CTA waits for in vain
+  int32_t stall;
 };
 // Bytes of partial results the launch of these sizes uses.
 size_t kv8_attention_partial_bytes(int32_t heads, int32_t dim, int32_t group, int32_t n,

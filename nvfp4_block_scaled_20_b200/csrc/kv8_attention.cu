@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(kDim, kTiles))
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kDepth; ++i) {
-      bar_init(smem_addr(&sm.full[i]), 1);
+      bar_init(smem_addr(&sm.full[i]), i == 0 ? 1 + a.stall : 1);
       bar_init(smem_addr(&sm.empty[i]), kWarps);
     }
     sm.gave_up = 0;
@@ -268,16 +268,15 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(kDim, kTiles))
         const bool mine_now = lane >= from && lane < from + pieces;
         const uint32_t here = __ballot_sync(0xFFFFFFFFu, mine_now && page >= 0);
         const uint32_t full = smem_addr(&sm.full[st]);
-        const bool stalled = a.stall && issued == 0;  // test hook: never announced nor copied
         if (mine_now) {
           const int p = lane - from;
           const float2 sc = make_float2(ks, vs);
           for (int k = 0; k < per_piece; ++k) sm.scale[st][p * per_piece + k] = sc;
         }
         __syncwarp();
-        if (lane == 0 && !stalled) bar_expect(full, __popc(here) * 2 * piece_bytes);
+        if (lane == 0) bar_expect(full, __popc(here) * 2 * piece_bytes);
         __syncwarp();
-        if (mine_now && page >= 0 && !stalled) {
+        if (mine_now && page >= 0) {
           const int p = lane - from;
           const int key = step_at(steps, i) * kStepKeys + p * piece_keys;
           const int64_t off = ((page * a.c.heads + head) * pt + key % pt) * kDim;

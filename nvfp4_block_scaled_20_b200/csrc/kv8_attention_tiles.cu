@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRaw; ++i) {
-      bar_init(smem_addr(&sm.raw_full[i]), 1);
+      bar_init(smem_addr(&sm.raw_full[i]), i == 0 ? 1 + a.stall : 1);
       bar_init(smem_addr(&sm.raw_empty[i]), kLoadWarps);
     }
     for (int i = 0; i < kSlots; ++i) {
@@ -730,10 +730,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         ok = warp_wait(smem_addr(&sm.raw_empty[to]), ((n / kRaw) & 1) ^ 1, gave_up, a.wait_limit_ns);
         if (!ok) break;
         const uint32_t full = smem_addr(&sm.raw_full[to]);
-        const bool stalled = a.stall && n == 0;  // test hook: never announced nor copied
         // (the bytes may be counted down before they are announced: the phase
         // ends with the arrival below at the earliest)
-        if (mine && page >= 0 && !stalled)
+        if (mine && page >= 0)
           bulk_copy(smem_addr(raw) + to * (kTile / 2) + (lane - base) * piece_bytes,
                     a.c.codes[which] + ((int64_t)page * a.c.heads + unit.head) * piece_bytes,
                     piece_bytes, full);
@@ -760,7 +759,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
         __syncwarp();
-        if (lane == 0 && !stalled) bar_expect(full, __popc(here) * piece_bytes);
+        if (lane == 0) bar_expect(full, __popc(here) * piece_bytes);
       }
     }
     if (!ok) {

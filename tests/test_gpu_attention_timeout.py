@@ -2,8 +2,8 @@
 runs out is reported, and the device stays usable.
 
 As for the GEMM, a wait runs out on purpose without any fault: with the test hook
-on (nvfp4_set_test_stall) every CTA leaves out its first copy of codes, so that
-what waits for it gives up after the nvfp4_set_wait_limit bound.  The kernel must
+on (nvfp4_set_test_stall) the barrier of every CTA's first copy of codes never
+completes, so that what waits for it gives up after the nvfp4_set_wait_limit bound.  The kernel must
 record NVFP4_ERR_TIMEOUT, wait for the copies and products it issued, meet the
 other CTAs of its cluster, free its tensor memory and return; the next call with
 the same workspace gives the right result with no error recorded."""
