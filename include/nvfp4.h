@@ -540,8 +540,9 @@ typedef struct nvfp4_kv8_query {
  *   out = softmax(scale q K^T) V over the tokens a query sees, lens[s] = the
  *   sequence's tokens in the cache (the queries' own among them).
  * The codes enter the matrix products as they are (fp16, exact), the scales in
- * fp32 beside them; scores, maxima and sums in fp32; the softmax weights are
- * rounded to fp16 for the product with V.  A query that sees nothing gets
+ * fp32 beside them; scores, maxima and sums in fp32; the softmax weights, times
+ * V's scale, are rounded to fp16 for the product with V (those below 2^-25 of a
+ * row's largest to 0).  A query that sees nothing gets
  * zeros.  A NaN among a token's keys makes the queries that see the token NaN and
  * reaches no others.  A NaN among its values makes that element NaN in the queries
  * that see the token, and possibly (0 * NaN) in queries that do not, but share a

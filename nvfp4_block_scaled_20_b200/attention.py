@@ -7,6 +7,12 @@ the tensors' device, or to ``stream``.  What a call allocates itself belongs to
 the stream it works on; tensors that it is given are ordered by the caller, as
 for any other work on two streams.
 
+What is wrong in device values (lengths, rows, pages that do not fit) shows in the
+workspace's error word, nvfp4_get_device_error / device_error(ws), and nowhere
+else: such sequences are skipped.  A call without ``ws`` takes a workspace that it
+drops, and its error word with it.  Rows of no sequence, and of skipped ones, are
+left as they are; in outputs that the call allocates they hold anything.
+
 These calls are made once per layer and token, so the host side is kept short:
 the C structs are packed with ``struct`` (the formats below) instead of being
 built field by field.

@@ -10,11 +10,20 @@
 //
 // ks_j, vs_j are the scales of j's page and head.  With V's scale inside the
 // exponent the value codes enter the matrix product as they are, at no
-// operation per element, and every weight is at most 2^kLazy whatever the
-// spread of V's scales, so fp16 weights lose nothing to range; log2(vs) is a
-// whole number.  The row sum divides a page's sum of weights by vs once.  With
-// |log2 vs| <= 40 a weight that underflows fp32 (2^-126) belongs to a
-// probability below 2^-46 of the row's largest.
+// operation per element; log2(vs) is a whole number.  The row sum divides a
+// page's sum of weights by vs once.  With |log2 vs| <= 40 a weight that underflows
+// fp32 (2^-126) belongs to a probability below 2^-46 of the row's largest.
+//
+// The weights are rounded to fp16 for the product with V, the one rounding below
+// 32 bits: the tensor cores take both operands in 16 bits at full rate, the codes
+// are exact in fp16, and its half step of 2^-11 stays well under that of the bf16
+// output (2^-8): the error against 64 bits is 1.66e-3 of the output in either case
+// (a bf16 weight's own half step would be 2^-8 too).  No weight overflows
+// (kLazy, kJump).  One below 2^-25 becomes 0 in the product, while the row sum,
+// in fp32, still counts it: what such a key adds, at most 448 * 2^-25 value codes
+// of the row's largest s_v exp(score), is lost.  That is 2^-7 of the smallest
+// code's step for each; it only shows where many keys' s_v is smaller than that
+// by 2^10 and more.
 #pragma once
 
 #include <cstdint>
@@ -161,9 +170,10 @@ __device__ __forceinline__ int step_at(const Steps& s, int i) {
   return i < s.head ? i : s.from + (i - s.head);
 }
 
-// The power of two that brings a query row of largest magnitude amax below 4
-// (its fp16 values then keep all bits of bf16 down to 2^-24 of the row's
-// largest), as an exponent.
+// The power of two that brings a query row of largest magnitude amax into [1, 2), as
+// an exponent.  In fp16 its values then keep all eight bits of bf16 down to 2^-17;
+// smaller ones are rounded to whole 2^-24, an error of at most 2^-25 of the row's
+// largest.
 __device__ __forceinline__ int row_exponent(float amax) {
   const int e = (int)(__float_as_uint(amax) >> 23) - 127;
   return max(-126, min(126, e));

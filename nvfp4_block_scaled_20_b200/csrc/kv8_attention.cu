@@ -503,6 +503,7 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(kDim, kTiles))
           p[2 + h] = exp2_approx(s[u][n][2 + h] - base[h]);
           l[n][h] = fmaf(p[h] + p[2 + h], inv, l[n][h]);
         }
+        // (to fp16: see attention_common.cuh; the sum above is of the fp32 weights)
         pf[u][n][0] = transposed(f16x2(p[0], p[1]));
         pf[u][n][1] = transposed(f16x2(p[2], p[3]));
       }

@@ -42,10 +42,13 @@
 // take as long as of 128: 1900), a quarter of the exponentials as polynomials
 // on the FMA pipe (packed fma: 3.6 clocks a warp; no change), CTAs that stay and
 // take the next tile by cluster launch control (they hide a tile's set-up and
-// look-ups, 0.5 us of 9, and cost registers in the steps: three prompts 439 for
-// 405, a chunk 1820 for 1720), counting the tiles of ragged sequences in the
-// kernel to split the true last round (three prompts 399 for 405, one prompt
-// 224 for 217, 40 short ones 1122 for 1095).
+// look-ups, 0.5 us of 9, and cost registers in the steps: three prompts 439 beside
+// 405 of the kernel at that time, a chunk 1820 beside 1720), counting the tiles of
+// ragged sequences in the kernel to split the true last round (three prompts 399
+// beside 405 at that time, one prompt 224 beside 217, 40 short ones 1122 beside
+// 1095; today's three prompts take 399 without), and taking NaN codes out of V in
+// steps that only some rows see, to set them in those rows at the end (the
+// converters are at their rate: three prompts 426 beside 400).
 //
 // Tensor memory (columns): S / P of the halves at 0 and 128, O at 256 and 384.
 #include <climits>
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             x0 = exp2_approx(x0);
             x1 = exp2_approx(x1);
             sum = add2(sum, pack2(x0, x1));
-            p[k] = f16x2(x0, x1);
+            p[k] = f16x2(x0, x1);  // (see attention_common.cuh; the sum is of the fp32 weights)
           }
           st16(ts + 16 * c, p);
           float a0, a1;

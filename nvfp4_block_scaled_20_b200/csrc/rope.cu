@@ -14,7 +14,9 @@
 //
 // The angle in turns is a double product: position * rate reaches 10^4..10^5
 // turns, where fp32 would keep 2^-8 of a turn.  Its fraction, exact, is
-// rounded to fp32 once and goes through sincospif.
+// rounded to fp32 once and goes through sincospif: 2^-26 of a turn, 9.4e-8 rad, no
+// more than the rounding of the fp32 products that follow (fp32 gradient against
+// 64 bits 4.1e-8 of its norm; with sine and cosine in 64 bits 3.75e-8).
 //
 // Measured (device time): q and k of 4680 tokens, 24 heads of 128, bf16: 23.3 us
 // for 115 MB, 4.9 TB/s; the fp32 gradient of 2641 tokens, 20 heads of 128: 8.9
@@ -54,15 +56,15 @@ struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Vec {
   T v[N];
 };
 
-// P pairs per thread step.  Interleaved: elements [2i, 2i + 2P), one vector;
-// halves: elements [i, i + P) and [i + pairs, i + pairs + P), two vectors; past
-// the rotated pairs both copy elements [2i, 2i + 2P).
 struct RopeLaunch {
   int tokens;     // per CTA
   int cols_inv;   // 65536 / d + 1 of the pairs of a head,
   int units_inv;  // and of the threads of a head
 };
 
+// P pairs per thread step.  Interleaved: elements [2i, 2i + 2P), one vector;
+// halves: elements [i, i + P) and [i + pairs, i + pairs + P), two vectors; past
+// the rotated pairs both copy elements [2i, 2i + 2P).
 template <typename T, bool kInterleaved, int P>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_kernel(const __grid_constant__ RopeArgs a, const RopeLaunch d) {
