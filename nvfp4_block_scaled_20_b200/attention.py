@@ -4,8 +4,9 @@ Torch-facing helpers of nvfp4_rope, nvfp4_kv8_write, nvfp4_kv8_read and
 nvfp4_kv8_attention (include/nvfp4.h): they check shapes and types, allocate
 outputs and marshal pointers and streams.  Work goes to the current stream of
 the tensors' device, or to ``stream``.  What a call allocates itself belongs to
-the stream it works on; tensors that it is given are ordered by the caller, as
-for any other work on two streams.
+the stream it works on (an output may be dropped while the caller's current stream
+still reads it); tensors that it is given are ordered by the caller, as for any
+other work on two streams.
 
 What is wrong in device values (lengths, rows, pages that do not fit) shows in the
 workspace's error word, nvfp4_get_device_error / device_error(ws), and nowhere
@@ -97,15 +98,22 @@ def _type(kind):
     raise TypeError("unsupported dtype %s" % kind)
 
 
-def _on(stream, index, call, *args):
+def _on(stream, index, given, call, *args):
     """call(*args) with `stream` current: the workspace and the outputs that it
     allocates then belong to that stream -- their first use is ordered after
-    whatever had the memory before, and so is what gets it next."""
+    whatever had the memory before, and so is what gets it next.  Outputs that
+    were not `given` are noted as in use by the caller's stream too, which has yet
+    to read them when they are dropped."""
     torch is None and _need_torch()
     if stream.device.index != index:
         raise ValueError("the stream is of another device than the tensors")
+    caller = torch.cuda.current_stream(index)
     with torch.cuda.stream(stream):
-        return call(*args)
+        outs = call(*args)
+    if not given:
+        for t in outs if isinstance(outs, (list, tuple)) else (outs,):
+            t.record_stream(caller)
+    return outs
 
 
 def _call(fn, index, *args):
@@ -179,8 +187,8 @@ def rope(xs, positions, sections, theta=10000.0, interleaved=True, per_axis=True
     type, strided) turned by positions (int32 [tokens, axes]).  With ``inverse``
     the gradients of xs from those of the outputs.  outs may be xs (in place)."""
     if stream is not None:
-        return _on(stream, positions.get_device(), rope, xs, positions, sections, theta, interleaved,
-                   per_axis, inverse, outs)
+        return _on(stream, positions.get_device(), outs is not None, rope, xs, positions, sections,
+                   theta, interleaved, per_axis, inverse, outs)
     torch is None and _need_torch()
     n, axes = len(xs), len(sections)
     if not 1 <= n <= 8 or not 1 <= axes <= 4:
@@ -237,7 +245,8 @@ def kv8_write(cache, k, v, page_table, lens, starts, max_new=None, ws=None, stre
     heads, head_dim]) become sequence s's tokens from lens[s] on.  max_new: at
     least the most rows of a sequence (default: all rows)."""
     if stream is not None:
-        return _on(stream, cache.index, kv8_write, cache, k, v, page_table, lens, starts, max_new, ws)
+        return _on(stream, cache.index, True, kv8_write, cache, k, v, page_table, lens, starts,
+                   max_new, ws)
     torch is None and _need_torch()
     rows = k.shape[0]
     kt, kh, vt, vh = _rows_of_cache(k, v, rows, cache)
@@ -252,8 +261,8 @@ def kv8_read(cache, page_table, begins, starts, rows, max_tokens=None, out_dtype
     """One nvfp4_kv8_read call: sequence s's tokens from begins[s] on become rows
     starts[s]..starts[s+1] of the returned (k, v), [rows, heads, head_dim]."""
     if stream is not None:
-        return _on(stream, cache.index, kv8_read, cache, page_table, begins, starts, rows, max_tokens,
-                   out_dtype, outs, ws)
+        return _on(stream, cache.index, outs is not None, kv8_read, cache, page_table, begins, starts,
+                   rows, max_tokens, out_dtype, outs, ws)
     torch is None and _need_torch()
     if outs is None:
         kind = out_dtype or torch.bfloat16
@@ -289,8 +298,8 @@ def kv8_attention(q, cache, page_table, lens, starts, max_q=None, scale=None, ca
     max_q: at least the most queries of a sequence (default: all rows).  lse: an
     fp32 [rows, q_heads] tensor that receives the log-sum-exps."""
     if stream is not None:
-        return _on(stream, cache.index, kv8_attention, q, cache, page_table, lens, starts, max_q,
-                   scale, causal, window, sink, out, lse, ws)
+        return _on(stream, cache.index, out is not None, kv8_attention, q, cache, page_table, lens,
+                   starts, max_q, scale, causal, window, sink, out, lse, ws)
     torch is None and _need_torch()
     if q.dtype is not torch.bfloat16:
         raise TypeError("q and out are bfloat16")

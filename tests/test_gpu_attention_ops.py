@@ -756,3 +756,38 @@ def test_attention_nan_values_stay_in_their_element_and_tile(nq, n, hq, hk, d, p
     assert torch.equal(out[~may], clean[~may])
     assert (out[may].isnan() | (out[may] == clean[may])).all()
     assert torch.equal(lse[0], lse[1])
+
+
+@pytest.mark.parametrize("call", ["token", "chunk", "read", "rope"])
+def test_outputs_dropped_while_the_callers_stream_still_reads_them(call):
+    """Calls on a stream of their own, one after the other, whose outputs another
+    stream reads late and that are dropped before: none gets the memory of one that
+    has yet to be read."""
+    heads, d, n = 2, 128, 900
+    c = filled(16, heads, 64, d, 161)
+    t = torch.arange(15, device=DEV, dtype=torch.int32)[None].contiguous()
+    nq = 1 if call == "token" else 300
+    xs = [torch.randn((nq, heads, d), generator=gen(162 + i), device=DEV).bfloat16() for i in range(4)]
+    lens, starts, begins = i32([n]), i32([0, nq]), [i32([100 * i]) for i in range(4)]
+    pos = torch.arange(nq, device=DEV, dtype=torch.int32)[:, None].contiguous()
+
+    def go(i, stream=None):
+        if call == "read":
+            return nv.kv8_read(c, t, begins[i], starts, nq, stream=stream)
+        if call == "rope":
+            return nv.rope([xs[i]], pos, [64], stream=stream)
+        return [nv.kv8_attention(xs[i], c, t, lens, starts, stream=stream)]
+
+    want = [[o.clone() for o in go(i)] for i in range(4)]
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    torch.cuda.synchronize()
+    late = []
+    for i in range(4):
+        outs = go(i, side)
+        here.wait_stream(side)
+        torch.cuda._sleep(5_000_000)
+        late.append([o.clone() for o in outs])
+        del outs
+    torch.cuda.synchronize()
+    for a, b in zip(late, want):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
