@@ -515,7 +515,8 @@ NVFP4_API nvfp4_status nvfp4_kv8_read(const nvfp4_kv8_cache* cache, const nvfp4_
 /* Queries of an attention call.
  *   q, out   device bf16 [rows, q_heads, head_dim], strides in elements
  *            (multiples of 8; the rows of out lie apart), 16-byte aligned;
- *            q_heads a multiple of the cache's heads (query head h reads KV head h / (q_heads / heads)).
+ *            q_heads a multiple of the cache's heads (query head h reads KV
+ *            head h / (q_heads / heads)).
  *   lse      device fp32 [rows, q_heads] or NULL: log of the sum of the
  *            exponentials (natural), -infinity for a row that sees nothing.
  *   scale    of the scores, > 0 (1 / sqrt(head_dim) as a rule).
@@ -542,8 +543,7 @@ typedef struct nvfp4_kv8_query {
  * The codes enter the matrix products as they are (fp16, exact), the scales in
  * fp32 beside them; scores, maxima and sums in fp32; the softmax weights, times
  * V's scale, are rounded to fp16 for the product with V (those below 2^-25 of a
- * row's largest to 0).  A query that sees nothing gets
- * zeros.  A NaN among a token's keys makes the queries that see the token NaN and
+ * row's largest to 0).  A query that sees nothing gets zeros.  A NaN among a token's keys makes the queries that see the token NaN and
  * reaches no others.  A NaN among its values makes that element NaN in the queries
  * that see the token, and possibly (0 * NaN) in queries that do not, but share a
  * tile with one that does: 256 rows of one sequence and KV head, a row being a
@@ -555,7 +555,9 @@ typedef struct nvfp4_kv8_query {
  * workspace.
  * Sizes: at most 2^30 tiles of 256 rows (queries times q_heads / heads) over all
  * sequences and KV heads, and for at most 48 rows a sequence at most 65535 KV
- * heads times tiles of 16 rows.  Waits are bounded (nvfp4_set_wait_limit). */
+ * heads times tiles of 16 rows.  max_rows chooses the kernel for the whole call:
+ * long prompts and single tokens are faster in calls of their own.  Waits are
+ * bounded (nvfp4_set_wait_limit). */
 NVFP4_API nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache,
                                            const nvfp4_kv8_batch* batch,
                                            const nvfp4_kv8_query* query, void* workspace,
@@ -615,8 +617,8 @@ NVFP4_API nvfp4_status nvfp4_set_wait_limit(uint64_t ns);
  * codes is waited for in vain while it and the following ones arrive.
  * The wait runs out after the nvfp4_set_wait_limit bound and the kernel takes its
  * abort path (NVFP4_ERR_TIMEOUT in the error word; a GEMM's output is not
- * written, an attention's is not to be used).  on = 0 (the default) turns it off; other values return
- * NVFP4_ERR_INVALID_ARG. */
+ * written, an attention's is not to be used).  on = 0 (the default) turns it
+ * off; other values return NVFP4_ERR_INVALID_ARG. */
 NVFP4_API nvfp4_status nvfp4_set_test_stall(int32_t on);
 
 /* ------------------------------------------------------------ status ---- */

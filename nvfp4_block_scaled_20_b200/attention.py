@@ -295,8 +295,9 @@ def kv8_attention(q, cache, page_table, lens, starts, max_q=None, scale=None, ca
                   window=-1, sink=0, out=None, lse=None, ws=None, stream=None):
     """One nvfp4_kv8_attention call: q bf16 [rows, q_heads, head_dim], sequence
     s's queries in rows starts[s]..starts[s+1], over its lens[s] cached tokens.
-    max_q: at least the most queries of a sequence (default: all rows).  lse: an
-    fp32 [rows, q_heads] tensor that receives the log-sum-exps."""
+    max_q: at least the most queries of a sequence (default: all rows); it chooses
+    the kernel for all of them, so prompts and single tokens are faster in calls of
+    their own.  lse: an fp32 [rows, q_heads] tensor that receives the log-sum-exps."""
     if stream is not None:
         return _on(stream, cache.index, out is not None, kv8_attention, q, cache, page_table, lens,
                    starts, max_q, scale, causal, window, sink, out, lse, ws)
