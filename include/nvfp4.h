@@ -462,7 +462,8 @@ typedef struct nvfp4_kv8_cache {
  * [starts[s], starts[s + 1]) of the call's tensors; rows past starts[n] belong
  * to none and are left as they are.
  *   page_table  device int32, table_pages entries per sequence; entries past a
- *               sequence's tokens are not read.
+ *               sequence's tokens are not read, nor are, by an attention, those of
+ *               pages that no query sees (their pages may be in use elsewhere).
  *   lens        device int32 [n]; its meaning is the call's.
  *   starts      device int32 [n + 1], from any first row on, not decreasing.
  *   rows        rows of the packed tensors.

@@ -150,6 +150,11 @@ __device__ __forceinline__ Seen seen_at(const Kv8Attention& a, int len, int at) 
 __device__ __forceinline__ Seen seen_by(const Kv8Attention& a, const QuerySeq& q, int i) {
   return seen_at(a, q.len, q.len - q.n + i);
 }
+// Whether some query sees one of keys [key, end), of queries whose first and last
+// see these.  (From query to query the limits only move up, by one.)
+__device__ __forceinline__ bool any_seen(const Seen& first, const Seen& last, int key, int end) {
+  return (key < last.hi && end > first.lo) || key < last.sink;
+}
 // Steps of kKeys keys that queries [i0, i1] of a sequence need: `head` steps
 // from 0 (the sink) and then those from `from` on, `total` in all.
 struct Steps {

@@ -236,6 +236,8 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(kDim, kTiles))
     const int piece_keys = kStepKeys / pieces;
     const uint32_t piece_bytes = piece_keys * kDim;
     const int per_piece = piece_keys / 32;
+    const Seen first = seen_by(a, q, row0 / a.group);
+    const Seen last = seen_by(a, q, (min(row0 + kRowsCta, rows) - 1) / a.group);
     bool ok = true;
     int issued = 0;
     for (int i0 = s0; i0 < s1 && ok; i0 += 32 / pieces) {
@@ -245,8 +247,9 @@ __global__ void __launch_bounds__(kRowThreads, ctas_per_sm(kDim, kTiles))
       float ks = 0.0f, vs = -1.0f;
       if (mine < s1) {
         const int key = step_at(steps, mine) * kStepKeys + (lane % pieces) * piece_keys;
-        // pages past the sequence's end are not looked up
-        if (key < q.len) {
+        // pages of keys that no row sees are not looked up: past the sequence's
+        // end, or out of the window, they may be gone
+        if (any_seen(first, last, key, key + piece_keys)) {
           page = a.b.table[seq * a.b.table_stride + key / pt];
           if (page < 0 || page >= a.c.pages) {
             atomicOr(a.err, kDevErrShape);

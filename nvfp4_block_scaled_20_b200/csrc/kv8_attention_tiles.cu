@@ -324,12 +324,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   // `step` on.  The first is on the way while the others set up.
   const int pt_log = 31 - __clz(pt);  // 5, 6 or 7
   const int step_log = 7 - pt_log;    // pages per step, as a power of two
+  const Seen first = seen_by(a, q, i_first), last = seen_by(a, q, i_last);
   auto fetch_page = [&](int step) {
     const int mine = step + (lane >> step_log);
     if (mine >= s1) return kNoPage;
     const int key = step_at(steps, mine) * kKeys + ((lane & ((1 << step_log) - 1)) << pt_log);
-    // pages past the sequence's end are not looked up
-    return key < q.len ? a.b.table[unit.seq * a.b.table_stride + (key >> pt_log)] : kNoPage;
+    // pages of keys that no row sees are not looked up: past the sequence's end, or
+    // out of the window, they may be gone
+    return any_seen(first, last, key, key + pt)
+               ? a.b.table[unit.seq * a.b.table_stride + (key >> pt_log)]
+               : kNoPage;
   };
   int next_page = kNoPage;
   if (warp == kCopyWarp) next_page = fetch_page(s0);
@@ -635,7 +639,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // rows.  The lanes' columns 4..7 go to the upper half of the warp.
     const int row = w * (32 / kLanesRow) + (kDim == 128 ? (lane >> 2) & 3 : lane >> 2);
     const int col = (lane & 3) + (kDim == 128 ? (lane >> 4) * 4 : 0);
-    const Seen first = seen_by(a, q, i_first), last = seen_by(a, q, i_last);
     bool ok = true;
     for (int n = 0; n < 2 * n_steps; ++n) {
       const int slot = n % kSlots, from = n % kRaw, j = n >> 1;
@@ -689,7 +692,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     // ------------------------------------------------------------------ copies
     const int pieces = 1 << step_log, group = 32 >> step_log;  // pages per step, steps per look-up
     const uint32_t piece_bytes = (uint32_t)pt * kDim;
-    const Seen first = seen_by(a, q, i_first), last = seen_by(a, q, i_last);
     // Each lane holds one of the next 32 pages and its scales; the following
     // ones are on the way, the scales a step after the pages: a look-up is two
     // dependent loads from memory, longer than a step.

@@ -791,3 +791,31 @@ def test_outputs_dropped_while_the_callers_stream_still_reads_them(call):
     torch.cuda.synchronize()
     for a, b in zip(late, want):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("nq,n,hq,hk", [(1, 1500, 4, 4), (5, 1000, 12, 2), (40, 2000, 4, 2), (300, 3000, 2, 1),
+                                        (700, 9000, 4, 2)])
+@pytest.mark.parametrize("pt,d", [(32, 64), (64, 64), (128, 64), (32, 128), (64, 128), (128, 128)])
+@pytest.mark.parametrize("window,sink", [(100, 0), (333, 40), (0, 70)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_pages_out_of_the_window_may_be_gone(nq, n, hq, hk, pt, d, window, sink, causal):
+    """Pages between the sink and the window of the first query may be freed: their
+    entries name none, or one that is full of NaN, and no error is recorded."""
+    mask = dict(causal=causal, window=window, sink=sink)
+    pages = -(-n // pt)
+    c = filled(pages + 1, hk, pt, d, 171)
+    for codes in (c.k_codes, c.v_codes):
+        codes[pages].fill_(0x7F)
+    t = torch.randperm(pages, generator=gen(172), device=DEV).to(torch.int32)[None].contiguous()
+    q = torch.randn((nq, hq, d), generator=gen(173), device=DEV).bfloat16()
+    lens, starts = i32([n]), i32([0, nq])
+    ws = nv.kv8_attention_workspace(c, t, starts, hq, nq)
+    want = nv.kv8_attention(q, c, t, lens, starts, ws=ws, **mask)
+    seen = ref.seen(nq, n, causal, window, sink, DEV).any(0)
+    unseen = ~torch.nn.functional.pad(seen, (0, pages * pt - n)).view(pages, pt).any(1)
+    assert unseen.any()
+    for gone in (-1, pages, 2 ** 31 - 1, c.k_codes.shape[0]):
+        less = torch.where(unseen[None], torch.full_like(t, gone), t)
+        out = nv.kv8_attention(q, c, less, lens, starts, ws=ws, **mask)
+        assert nv.device_error(ws) == 0
+        assert torch.equal(out, want)
