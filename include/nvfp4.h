@@ -468,6 +468,7 @@ typedef struct nvfp4_kv8_cache {
  *   starts      device int32 [n + 1], from any first row on, not decreasing.
  *   rows        rows of the packed tensors.
  *   max_rows    at least the rows of every sequence (host; sizes the launch).
+ *   n           may be 0 (no work; the arrays may then be NULL).
  * Device values are checked on the device: a sequence whose rows or tokens do
  * not fit (rows, max_rows, table_pages) is skipped, and so is a page outside
  * the cache, and NVFP4_ERR_SHAPE is recorded in the workspace error word. */
@@ -517,7 +518,8 @@ NVFP4_API nvfp4_status nvfp4_kv8_read(const nvfp4_kv8_cache* cache, const nvfp4_
  *   q, out   device bf16 [rows, q_heads, head_dim], strides in elements
  *            (multiples of 8; the rows of out lie apart), 16-byte aligned;
  *            q_heads a multiple of the cache's heads (query head h reads KV
- *            head h / (q_heads / heads)).
+ *            head h / (q_heads / heads)).  out may be q itself, with the same
+ *            strides; they do not overlap otherwise.
  *   lse      device fp32 [rows, q_heads] or NULL: log of the sum of the
  *            exponentials (natural), -infinity for a row that sees nothing.
  *   scale    of the scores, > 0 (1 / sqrt(head_dim) as a rule).

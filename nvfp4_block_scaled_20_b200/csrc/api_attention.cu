@@ -46,7 +46,9 @@ nvfp4_status check_cache(const nvfp4_kv8_cache* c) {
 }
 
 nvfp4_status check_batch(const nvfp4_kv8_batch* b, int32_t page_tokens) {
-  if (!b || !b->page_table || !b->lens || !b->starts) return NVFP4_ERR_INVALID_ARG;
+  if (!b) return NVFP4_ERR_INVALID_ARG;
+  // (arrays of no sequences have no address)
+  if (b->n != 0 && (!b->page_table || !b->lens || !b->starts)) return NVFP4_ERR_INVALID_ARG;
   // sequences are a grid dimension; token positions are 32-bit
   if (b->n < 0 || b->n > 65535 || b->rows < 0 || b->max_rows < 0 || b->table_pages < 1 ||
       b->table_stride < b->table_pages)
@@ -240,6 +242,10 @@ nvfp4_status nvfp4_kv8_attention(const nvfp4_kv8_cache* cache, const nvfp4_kv8_b
   if (!rows_apart(batch->rows, qp->out_token_stride, qp->q_heads, qp->out_head_stride,
                   cache->head_dim))
     return NVFP4_ERR_SHAPE;
+  // a tile reads its rows of q before it writes any of them
+  if (qp->out == qp->q && ((batch->rows > 1 && qp->out_token_stride != qp->q_token_stride) ||
+                           (qp->q_heads > 1 && qp->out_head_stride != qp->q_head_stride)))
+    return NVFP4_ERR_INVALID_ARG;
   Kv8Attention a;
   std::memset(&a, 0, sizeof(a));
   a.c = cache_of(cache);

@@ -316,6 +316,12 @@ def test_outputs_whose_rows_overlap_are_refused():
     for v, want in ((A, INVALID), (2 * A, SHAPE)):
         assert capi.nvfp4_kv8_read(many["cache"], many["batch"], 1, A, *wide, v, *wide, A, ws,
                                    None) == want
+    # in place of q, but at other strides
+    same = dict(q=A, out=A, lse=None, q_heads=8, out_token_stride=1024, out_head_stride=128, scale=0.1,
+                causal=1, window=-1, sink=0)
+    for tq, hq, want in ((1024, 128, WORKSPACE), (2048, 128, INVALID), (1024, 256, INVALID)):
+        query = capi.nvfp4_kv8_query(q_token_stride=tq, q_head_stride=hq, **same)
+        assert capi.nvfp4_kv8_attention(_cache(), _batch(), query, None, ws, None) == want
     # one token, one head: a stride that is not used may be anything
     assert _rope(out=2 * A, heads=8, tokens=1, strides=(0, 0, 0, 128), pos=None) == INVALID
     assert _rope(out=2 * A, heads=1, tokens=6, strides=(0, 0, 128, 0), pos=None) == INVALID
@@ -336,3 +342,12 @@ def test_rope_refuses_outputs_in_the_place_of_other_tensors():
     assert go((A, 3 * A, 1024), (2 * A, 3 * A, 1024)) == INVALID
     assert go((A, A, 1024), (A, 2 * A, 1024)) == INVALID
     assert go((A, A, 2048)) == INVALID
+
+
+def test_a_batch_of_no_sequences_is_no_work():
+    """As empty tensors have it: arrays without an address."""
+    none = _batch(n=0, rows=0, max_rows=0, page_table=None, lens=None, starts=None)
+    query = capi.nvfp4_kv8_query(q=None, out=None, lse=None, q_heads=8, scale=0.1, causal=1, window=-1)
+    assert capi.nvfp4_kv8_write(_cache(), none, 1, None, 0, 0, None, 0, 0, None, 0, None) == OK
+    assert capi.nvfp4_kv8_read(_cache(), none, 1, None, 0, 0, None, 0, 0, None, 0, None) == OK
+    assert capi.nvfp4_kv8_attention(_cache(), none, query, None, 0, None) == OK

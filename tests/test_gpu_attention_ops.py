@@ -819,3 +819,49 @@ def test_attention_pages_out_of_the_window_may_be_gone(nq, n, hq, hk, pt, d, win
         out = nv.kv8_attention(q, c, less, lens, starts, ws=ws, **mask)
         assert nv.device_error(ws) == 0
         assert torch.equal(out, want)
+
+
+def test_no_sequences_no_rows_no_tokens():
+    """Empty batches, and batches whose sequences have no rows, do nothing."""
+    c = filled(4, 2, 64, 128, 181)
+    kept = [x.clone() for x in (c.k_codes, c.v_codes, c.k_scales, c.v_scales)]
+    x = torch.randn((0, 2, 128), device=DEV).bfloat16()
+    for n in (0, 1, 3):
+        t = torch.zeros((n, 2), dtype=torch.int32, device=DEV)
+        lens, starts = i32([5] * n), i32([0] * (n + 1))
+        ws = nv.kv8_attention_workspace(c, t, starts, 4, 1)
+        nv.kv8_write(c, x, x, t, lens, starts, ws=ws)
+        k, v = nv.kv8_read(c, t, lens, starts, 0, ws=ws)
+        assert k.shape == v.shape == (0, 2, 128)
+        q = torch.randn((0, 4, 128), device=DEV).bfloat16()
+        assert nv.kv8_attention(q, c, t, lens, starts).shape == (0, 4, 128)
+        # rows that belong to no sequence
+        y = torch.randn((7, 2, 128), generator=gen(182), device=DEV).bfloat16()
+        nv.kv8_write(c, y, y, t, lens, starts, ws=ws)
+        outs = [torch.full_like(y, 4.0) for _ in "kv"]
+        nv.kv8_read(c, t, lens, starts, 7, outs=outs, ws=ws)
+        out = torch.full((7, 4, 128), 4.0, device=DEV).bfloat16()
+        nv.kv8_attention(torch.zeros_like(out), c, t, lens, starts, max_q=7, out=out, lse=None)
+        assert all((o == 4.0).all() for o in (*outs, out))
+        assert nv.device_error(ws) == 0
+    pos = torch.zeros((0, 3), dtype=torch.int32, device=DEV)
+    assert nv.rope([x, x[:, :1]], pos, [22, 21, 21])[1].shape == (0, 1, 128)
+    for a, b in zip(kept, (c.k_codes, c.v_codes, c.k_scales, c.v_scales)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("nq,n", [(1, 200), (1, 1500), (2, 9000), (40, 700), (600, 2500)])
+def test_attention_in_place_of_q(nq, n):
+    """out may be q itself: a tile reads its rows before it writes any of them."""
+    hk, hq, d = 2, 6, 128
+    pages = -(-n // 64)
+    c = filled(pages, hk, 64, d, 183)
+    t = torch.arange(pages, device=DEV, dtype=torch.int32)[None].contiguous()
+    qkv = torch.randn((nq, hq + 2 * hk, d), generator=gen(184), device=DEV).bfloat16()
+    args = (c, t, i32([n]), i32([0, nq]))
+    before = qkv.clone()
+    want = nv.kv8_attention(qkv[:, :hq], *args, causal=True)
+    for _ in range(5):
+        qkv.copy_(before)
+        nv.kv8_attention(qkv[:, :hq], *args, causal=True, out=qkv[:, :hq])
+        assert torch.equal(qkv[:, :hq], want) and torch.equal(qkv[:, hq:], before[:, hq:])
