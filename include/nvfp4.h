@@ -495,8 +495,8 @@ typedef struct nvfp4_kv8_batch {
  * otherwise.
  *   k, v  device [rows, heads, head_dim] of dtype, strides in elements, 16-byte
  *         aligned rows.
- * A page may be written for one sequence only in a call (shared prefix pages
- * are read-only).  Deterministic; no atomics.
+ * A page may be written for one sequence only in a call, and in one place of its
+ * table (shared prefix pages are read-only).  Deterministic; no atomics.
  * Workspace: nvfp4_workspace_bytes(0) (the device error word), 4-byte aligned. */
 NVFP4_API nvfp4_status nvfp4_kv8_write(const nvfp4_kv8_cache* cache, const nvfp4_kv8_batch* batch,
                                        int32_t dtype, const void* k, int64_t k_token_stride,
